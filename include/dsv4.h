@@ -316,7 +316,111 @@ dsv4_status dsv4_grouped_out_proj(const dsv4_params* params, int32_t T, int32_t 
                                   int32_t hidden, const void* o, const void* wa, const void* wb, void* u,
                                   void* y, void* stream);
 
-/* Bytes of workspace any entry point needs for these params (a pure function of them). */
+/* Sizes of one call of the operators that follow the attention in a decoder layer: the
+ * residual stream's norm, the routing to experts and the experts' products.  The caller sets
+ * every field that the called entry point names. */
+typedef struct dsv4_moe_params {
+  int32_t T;            /* tokens */
+  int32_t hidden;       /* hidden_size */
+  int32_t inter;        /* moe_intermediate_size */
+  int32_t E;            /* n_routed_experts */
+  int32_t topk;         /* num_experts_per_tok */
+  int32_t n_group;      /* groups of E / n_group consecutive experts (1: no groups) */
+  int32_t topk_group;   /* groups that a token may choose from */
+  int32_t score_fn;     /* dsv4_score_fn */
+  int32_t renorm;       /* norm_topk_prob: 1: the weights are divided by their sum */
+  int32_t scale_pow2;   /* 1: the scales of the 8-bit form are powers of two */
+  int32_t dtype;        /* dsv4_dtype of the activations */
+  int32_t logits_dtype; /* dsv4_dtype of the router logits */
+  float eps;            /* rms_norm_eps */
+  float routed_scale;   /* routed_scaling_factor */
+  float swiglu_limit;   /* swiglu_limit; 0: no clamp */
+} dsv4_moe_params;
+
+typedef enum { DSV4_SCORE_SOFTMAX = 0, DSV4_SCORE_SIGMOID = 1, DSV4_SCORE_SQRT_SOFTPLUS = 2 } dsv4_score_fn;
+
+/*
+ * Residual addition and root-mean-square norm of each token's row, with an optional 8-bit
+ * form of the result (the layer's norms, before the attention and before the experts):
+ *   r = x + residual,   y = r / sqrt(mean_c(r_c^2) + eps) * weight
+ *   s_g = max_{c in g} |y_c| / 448,   q_c = e4m3(y_c / s_g)      g: 128 consecutive channels
+ * r, its sum of squares and y are formed in 32 bits; r, y and q are each rounded once, from
+ * those.  The last group may be shorter than 128.  The scale of an all-zero group is 1; with
+ * scale_pow2 the scales are rounded up to a power of two (q * s is then exact in bf16).
+ * A NaN in a row makes the row NaN.
+ *
+ *   x         [T,hidden] T
+ *   residual  [T,hidden] T or NULL (r = x)
+ *   weight    [hidden] T
+ *   res_out   [T,hidden] T or NULL   out: r (may be x or residual itself)
+ *   y         [T,hidden] T or NULL   out (may be x or residual itself, not res_out)
+ *   yq        [T,hidden] e4m3 or NULL                out: q
+ *   yscale    [T,ceil(hidden/128)] f32, NULL without yq   out: s
+ * At least one of y and yq.  Uses T, hidden, eps, scale_pow2 and dtype.  Any hidden >= 1;
+ * rows of whole 16-byte pieces are read fastest.  Validates on the host (DSV4_ERR_ARG /
+ * _SHAPE / _ALIGN / _DTYPE) before any launch; allocates nothing.
+ */
+dsv4_status dsv4_add_rms_norm(const dsv4_moe_params* params, const void* x, const void* residual,
+                              const void* weight, void* res_out, void* y, void* yq, float* yscale, void* stream);
+
+/*
+ * Routing of tokens to experts ([V4] MoE: sqrt(softplus) scores with e_score_correction_bias;
+ * [V32]: sigmoid scores, n_group / topk_group, norm_topk_prob, routed_scaling_factor).
+ *   s_e = softmax(l)_e, 1 / (1 + exp(-l_e)) or sqrt(log(1 + exp(l_e)))       (score_fn)
+ *   c_e = s_e + bias_e
+ * Of the n_group groups of consecutive experts the topk_group with the largest sum of their
+ * two largest c stay (of their one c where a group is one expert); of their experts the topk
+ * with the largest c are chosen, in descending order of c.  Equal values go to the lower
+ * index.  weight_j = s of the j-th choice, divided by (the sum over the choices + 1e-20) with
+ * renorm, times routed_scale: the bias chooses, it does not weigh.
+ * The order is that of c in exact arithmetic: choices whose 32-bit values are too close to
+ * tell are decided in 64 bits.  A NaN c counts as -inf; a logit of -inf has score 0 (all
+ * logits -inf: all scores 0).
+ *
+ *   logits   [T,E] of logits_dtype
+ *   bias     [E] f32 or NULL
+ *   ids      [T,topk] int32   out
+ *   weights  [T,topk] f32     out
+ * Uses T, E (<= 1024), topk (<= 32, <= the experts of topk_group groups), n_group (<= 32, a
+ * divisor of E), topk_group, score_fn, renorm, routed_scale and logits_dtype.  Validates on
+ * the host before any launch; allocates nothing.
+ */
+dsv4_status dsv4_route_experts(const dsv4_moe_params* params, const void* logits, const float* bias, int32_t* ids,
+                               float* weights, void* stream);
+
+/*
+ * The experts' products of a routed layer ([V4] MoE, clamped SwiGLU: swiglu_limit):
+ *   out[t] = sum_j weights[t,j] * W2_e (silu(min(g, L)) * clamp(u, -L, L)),
+ *   g = W13_e[0:inter] x_t,   u = W13_e[inter:2*inter] x_t,   e = ids[t,j],  L = swiglu_limit
+ * (no clamp with swiglu_limit 0).  bf16 operands with fp32 accumulation; the product of silu
+ * and u is rounded to bf16, what is summed over j is kept in 32 bits.  A shared expert is one
+ * more column of ids and weights.
+ *
+ *   x         [T,hidden] bf16; or e4m3 when x_scale is given: x = q * s, rounded to bf16 (exact
+ *             where s is a power of two: dsv4_add_rms_norm with scale_pow2)
+ *   x_scale   [T,ceil(hidden/128)] f32 or NULL
+ *   ids       [T,topk] int32; a value outside 0 .. E-1 (-1: dropped) contributes nothing, an
+ *             expert named twice contributes twice
+ *   weights   [T,topk] f32
+ *   w13       [E,2*inter,hidden] bf16   gate rows, then up rows
+ *   w2        [E,hidden,inter] bf16
+ *   out       [T,hidden] bf16  (not x)
+ *   workspace, ws_bytes   >= dsv4_expert_mlp_workspace_bytes(params); 16-byte aligned; holds
+ *             nothing between calls, and two calls that overlap in time need one each
+ * Uses T, hidden and inter (multiples of 16), E (<= 1024), topk (<= 64, T * topk < 2^31),
+ * swiglu_limit and dtype (must be DSV4_BF16).  Validates on the host before any launch;
+ * allocates nothing.
+ */
+dsv4_status dsv4_expert_mlp(const dsv4_moe_params* params, const void* x, const float* x_scale, const int32_t* ids,
+                            const float* weights, const void* w13, const void* w2, void* out, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/* Bytes of workspace dsv4_expert_mlp needs (a pure function of T, hidden, inter, E and topk;
+ * 0 for sizes that it refuses). */
+size_t dsv4_expert_mlp_workspace_bytes(const dsv4_moe_params* params);
+
+/* Bytes of workspace any entry point that takes a dsv4_params needs for these params (a pure
+ * function of them). */
 size_t dsv4_workspace_bytes(const dsv4_params* params);
 
 /* Static, NUL-terminated description of a status code. */

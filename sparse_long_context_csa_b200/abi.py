@@ -22,7 +22,8 @@ EXPORTED = ("dsv4_compress_kv", "dsv4_indexer_topk", "dsv4_sparse_mqa_attn", "ds
             "dsv4_hca_layer", "dsv4_workspace_bytes", "dsv4_status_string", "dsv4_version",
             "dsv4_launch_count", "dsv4_indexer_topk_noalloc", "dsv4_device_check", "dsv4_indexer_scores",
             "dsv4_topk_select", "dsv4_decode_append", "dsv4_grouped_out_proj", "dsv4_set_index_checks",
-            "dsv4_index_checks", "dsv4_sparse_mqa_attn_scores")
+            "dsv4_index_checks", "dsv4_sparse_mqa_attn_scores", "dsv4_add_rms_norm", "dsv4_route_experts",
+            "dsv4_expert_mlp", "dsv4_expert_mlp_workspace_bytes")
 
 
 class Dsv4Error(RuntimeError):
@@ -41,6 +42,20 @@ class Dsv4Params(ctypes.Structure):
 
     def __repr__(self):
         return "Dsv4Params(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRT_SOFTPLUS = 0, 1, 2
+
+
+class Dsv4MoeParams(ctypes.Structure):
+    """Mirror of ``dsv4_moe_params`` (field order and types must match include/dsv4.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "hidden", "inter", "E", "topk", "n_group", "topk_group", "score_fn", "renorm", "scale_pow2",
+                 "dtype", "logits_dtype")] + \
+               [(n, ctypes.c_float) for n in ("eps", "routed_scale", "swiglu_limit")]
+
+    def __repr__(self):
+        return "Dsv4MoeParams(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
 _lib = None
@@ -67,6 +82,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsv4_csa_layer.argtypes = [P] + [vp] * 17 + [sz, vp]
     lib.dsv4_hca_layer.argtypes = [P] + [vp] * 10 + [sz, vp]
     lib.dsv4_grouped_out_proj.argtypes = [P, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    M = ctypes.POINTER(Dsv4MoeParams)
+    lib.dsv4_add_rms_norm.argtypes = [M] + [vp] * 8
+    lib.dsv4_route_experts.argtypes = [M] + [vp] * 5
+    lib.dsv4_expert_mlp.argtypes = [M] + [vp] * 8 + [sz, vp]
+    lib.dsv4_expert_mlp_workspace_bytes.argtypes = [M]
+    lib.dsv4_expert_mlp_workspace_bytes.restype = sz
     lib.dsv4_set_index_checks.argtypes = [i32]
     lib.dsv4_set_index_checks.restype = None
     lib.dsv4_index_checks.restype = i32
@@ -80,7 +101,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsv4_device_check.restype = ctypes.c_int
     for fn in ("dsv4_compress_kv", "dsv4_indexer_topk", "dsv4_sparse_mqa_attn", "dsv4_csa_layer",
                "dsv4_hca_layer", "dsv4_indexer_topk_noalloc", "dsv4_indexer_scores", "dsv4_topk_select",
-               "dsv4_decode_append", "dsv4_grouped_out_proj", "dsv4_sparse_mqa_attn_scores"):
+               "dsv4_decode_append", "dsv4_grouped_out_proj", "dsv4_sparse_mqa_attn_scores", "dsv4_add_rms_norm",
+               "dsv4_route_experts", "dsv4_expert_mlp"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -199,6 +221,32 @@ def dsv4_grouped_out_proj(params, T, groups, dg, hidden, o, wa, wb, u, y, stream
     _check("dsv4_grouped_out_proj",
            load().dsv4_grouped_out_proj(ctypes.byref(params), T, groups, dg, hidden, _ptr(o), _ptr(wa), _ptr(wb),
                                         _ptr(u), _ptr(y), _stream(stream)))
+
+
+def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=None, stream=None):
+    """r = x + residual (res_out), y = rms_norm(r) * weight, and y in e4m3 with a scale per 128 channels."""
+    _check("dsv4_add_rms_norm", load().dsv4_add_rms_norm(
+        ctypes.byref(params), _ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(y), _ptr(yq), _ptr(yscale),
+        _stream(stream)))
+
+
+def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
+    """The topk experts of each token (ids, in descending order of score + bias) and their weights."""
+    _check("dsv4_route_experts", load().dsv4_route_experts(
+        ctypes.byref(params), _ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), _stream(stream)))
+
+
+def dsv4_expert_mlp_workspace_bytes(params: Dsv4MoeParams) -> int:
+    return int(load().dsv4_expert_mlp_workspace_bytes(ctypes.byref(params)))
+
+
+def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, ws_bytes=None, stream=None):
+    """The weighted sum of each token's experts' clamped SwiGLU products."""
+    ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \
+        else (ws_bytes or 0)
+    _check("dsv4_expert_mlp", load().dsv4_expert_mlp(
+        ctypes.byref(params), _ptr(x), _ptr(x_scale), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w2), _ptr(out),
+        _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def dsv4_set_index_checks(on: bool) -> None:

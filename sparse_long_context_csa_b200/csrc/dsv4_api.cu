@@ -6,6 +6,7 @@
 #include <atomic>
 
 #include "internal.h"
+#include "moe.h"
 
 using namespace dsv4;
 
@@ -451,6 +452,87 @@ dsv4_status dsv4_grouped_out_proj(const dsv4_params* p, int32_t T, int32_t group
   a.o = o; a.wa = wa; a.wb = wb; a.u = u; a.y = y;
   if (!out_proj_supported(a)) return DSV4_ERR_SHAPE;
   return from_cuda(launch_out_proj(a, as_stream(stream)));
+}
+
+namespace {
+
+bool bad_flag(int32_t v) { return v != 0 && v != 1; }
+bool bad_dtype(int32_t v) { return v != DSV4_F32 && v != DSV4_BF16; }
+
+dsv4_status check_experts(const dsv4_moe_params* p) {
+  if (!p) return DSV4_ERR_ARG;
+  if (bad_dtype(p->dtype)) return DSV4_ERR_DTYPE;
+  if (p->dtype != DSV4_BF16) return DSV4_ERR_SHAPE;  // tensor-core operands
+  if (p->T < 0 || p->hidden < 16 || p->inter < 16 || p->hidden % 16 != 0 || p->inter % 16 != 0) return DSV4_ERR_SHAPE;
+  if (p->hidden > kMaxWidth || p->inter > kMaxWidth) return DSV4_ERR_SHAPE;
+  if (p->E < 1 || p->E > kMaxExperts || p->topk < 1 || p->topk > kMaxExpertTopk) return DSV4_ERR_SHAPE;
+  if ((int64_t)p->T * p->topk > INT32_MAX) return DSV4_ERR_SHAPE;
+  if (!(p->swiglu_limit >= 0.f)) return DSV4_ERR_ARG;
+  return DSV4_OK;
+}
+
+}  // namespace
+
+dsv4_status dsv4_add_rms_norm(const dsv4_moe_params* p, const void* x, const void* residual, const void* weight,
+                              void* res_out, void* y, void* yq, float* yscale, void* stream) {
+  if (!p) return DSV4_ERR_ARG;
+  if (bad_dtype(p->dtype)) return DSV4_ERR_DTYPE;
+  if (p->T < 0 || p->hidden < 1 || p->hidden > kMaxWidth) return DSV4_ERR_SHAPE;
+  if (!(p->eps >= 0.f) || bad_flag(p->scale_pow2)) return DSV4_ERR_ARG;
+  if (!x || !weight || (!y && !yq) || (yq && !yscale) || (!yq && yscale)) return DSV4_ERR_ARG;
+  const void* ptrs[] = {x, residual, weight, res_out, y, yq, yscale};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return DSV4_ERR_ALIGN;
+  if (res_out && res_out == y) return DSV4_ERR_ARG;
+  NormArgs a{};
+  a.T = p->T; a.hidden = p->hidden; a.scale_pow2 = p->scale_pow2; a.eps = p->eps;
+  a.x = x; a.residual = residual; a.weight = weight; a.res_out = res_out; a.y = y;
+  a.yq = static_cast<uint8_t*>(yq); a.yscale = yscale;
+  return from_cuda(launch_norm(a, p->dtype, as_stream(stream)));
+}
+
+dsv4_status dsv4_route_experts(const dsv4_moe_params* p, const void* logits, const float* bias, int32_t* ids,
+                               float* weights, void* stream) {
+  if (!p) return DSV4_ERR_ARG;
+  if (bad_dtype(p->logits_dtype)) return DSV4_ERR_DTYPE;
+  if (p->T < 0 || p->E < 1 || p->E > kMaxExperts || p->topk < 1 || p->topk > kMaxRouteTopk) return DSV4_ERR_SHAPE;
+  if (p->n_group < 1 || p->n_group > kMaxRouteGroups || p->E % p->n_group != 0) return DSV4_ERR_SHAPE;
+  if (p->topk_group < 1 || p->topk_group > p->n_group) return DSV4_ERR_SHAPE;
+  if (p->topk > p->topk_group * (p->E / p->n_group)) return DSV4_ERR_SHAPE;
+  if (p->score_fn < DSV4_SCORE_SOFTMAX || p->score_fn > DSV4_SCORE_SQRT_SOFTPLUS) return DSV4_ERR_ARG;
+  if (bad_flag(p->renorm) || !(p->routed_scale == p->routed_scale)) return DSV4_ERR_ARG;
+  if (!logits || !ids || !weights) return DSV4_ERR_ARG;
+  const void* ptrs[] = {logits, bias, ids, weights};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return DSV4_ERR_ALIGN;
+  RouteArgs a{};
+  a.T = p->T; a.E = p->E; a.topk = p->topk; a.n_group = p->n_group; a.topk_group = p->topk_group;
+  a.score_fn = p->score_fn; a.renorm = p->renorm; a.routed_scale = p->routed_scale;
+  a.logits = logits; a.bias = bias; a.ids = ids; a.weights = weights;
+  return from_cuda(launch_route(a, p->logits_dtype, as_stream(stream)));
+}
+
+size_t dsv4_expert_mlp_workspace_bytes(const dsv4_moe_params* p) {
+  if (check_experts(p) != DSV4_OK) return 0;
+  return expert_workspace_bytes(p->T, p->hidden, p->inter, p->E, p->topk);
+}
+
+dsv4_status dsv4_expert_mlp(const dsv4_moe_params* p, const void* x, const float* x_scale, const int32_t* ids,
+                            const float* weights, const void* w13, const void* w2, void* out, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  dsv4_status st = check_experts(p);
+  if (st != DSV4_OK) return st;
+  if (!x || !ids || !weights || !w13 || !w2 || !out || out == x) return DSV4_ERR_ARG;
+  const void* ptrs[] = {x, x_scale, ids, weights, w13, w2, out, workspace};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return DSV4_ERR_ALIGN;
+  if (p->T == 0) return DSV4_OK;
+  if (!workspace || ws_bytes < dsv4_expert_mlp_workspace_bytes(p)) return DSV4_ERR_WORKSPACE;
+  ExpertArgs a{};
+  a.T = p->T; a.hidden = p->hidden; a.inter = p->inter; a.E = p->E; a.topk = p->topk; a.limit = p->swiglu_limit;
+  a.x = x; a.x_scale = x_scale; a.ids = ids; a.weights = weights; a.w13 = w13; a.w2 = w2; a.out = out;
+  a.ws = workspace;
+  return from_cuda(launch_experts(a, as_stream(stream)));
 }
 
 }  // extern "C"
