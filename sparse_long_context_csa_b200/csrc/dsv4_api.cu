@@ -218,12 +218,13 @@ uint64_t dsv4_launch_count(void) { return g_launches.load(std::memory_order_rela
 
 dsv4_status dsv4_device_check(void* stream) {
   if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return DSV4_ERR_CUDA;
-  int code = 0, code2 = 0, code3 = 0, code4 = 0;
+  int code = 0, code2 = 0, code3 = 0, code4 = 0, code5 = 0;
   if (take_attn_tc_error(&code) != cudaSuccess) return DSV4_ERR_CUDA;
   if (take_indexer_tc_error(&code2) != cudaSuccess) return DSV4_ERR_CUDA;
   if (take_out_proj_error(&code3) != cudaSuccess) return DSV4_ERR_CUDA;
   if (take_index_check_error(&code4) != cudaSuccess) return DSV4_ERR_CUDA;
-  return (code || code2 || code3 || code4) ? DSV4_ERR_DEVICE_CHECK : DSV4_OK;
+  if (take_experts_error(&code5) != cudaSuccess) return DSV4_ERR_CUDA;
+  return (code || code2 || code3 || code4 || code5) ? DSV4_ERR_DEVICE_CHECK : DSV4_OK;
 }
 
 void dsv4_set_index_checks(int32_t on) { set_index_checks(on); }

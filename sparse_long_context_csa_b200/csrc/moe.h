@@ -58,5 +58,6 @@ struct ExpertArgs {
 };
 size_t expert_workspace_bytes(int64_t T, int hidden, int inter, int E, int topk);
 cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t st);
+cudaError_t take_experts_error(int* code);
 
 }  // namespace dsv4
