@@ -16,8 +16,12 @@ __device__ int g_experts_error = 0;
 
 namespace {
 
+// Chunks that the pairs are counted and placed in: one CTA each.
+constexpr int kMaxChunks = 64, kOrderThreads = 1024;
+constexpr int64_t kOneCta = 4096;  // pairs that a single CTA orders
+
 struct Layout {
-  size_t offs, row_slot, slot_row, h, yp, total;
+  size_t offs, row_slot, slot_row, counts, h, yp, total;
 };
 Layout layout(int64_t T, int hidden, int inter, int E, int topk) {
   const int64_t n = T * topk;
@@ -26,37 +30,101 @@ Layout layout(int64_t T, int hidden, int inter, int E, int topk) {
   l.offs = 0;
   l.row_slot = up((size_t)(E + 1) * 4);
   l.slot_row = l.row_slot + up((size_t)n * 4);
-  l.h = l.slot_row + up((size_t)n * 4);
+  l.counts = l.slot_row + up((size_t)n * 4);
+  l.h = l.counts + (n > kOneCta ? up((size_t)kMaxChunks * E * 4) : 0);
   l.yp = l.h + up((size_t)n * inter * 2);
   l.total = l.yp + up((size_t)n * hidden * 4);
   return l;
 }
 
-// One CTA: rows of the pairs in order of their expert.
-__global__ void __launch_bounds__(1024) order_kernel(const int32_t* ids, int64_t n, int E, int32_t* offs,
-                                                     int32_t* row_slot, int32_t* slot_row) {
-  __shared__ int32_t count[kMaxExperts], at[kMaxExperts];
-  for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
-  __syncthreads();
-  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+// A kernel that follows another one in the call waits here for what that one wrote (its launch
+// and its set-up overlap the other's end); the next one may be launched from the start.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ bool is_expert(int e, int E) { return e >= 0 && e < E; }
+
+// count[e] <- the sum of the counts before e, plus base(e); E <= kOrderThreads threads take part.
+__device__ __forceinline__ int exclusive_scan(int v, int* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
   }
+  if (lane == 31) part[warp] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int s = 0;
-    for (int e = 0; e < E; ++e) {
-      offs[e] = at[e] = s;
-      s += count[e];
+  if (warp == 0) {
+    int w = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
     }
-    offs[E] = s;
+    part[lane] = w;
   }
   __syncthreads();
-  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-    const int e = ids[i];
+  return s - v + (warp > 0 ? part[warp - 1] : 0);
+}
+
+// Pairs of chunk blockIdx.x by expert.
+__global__ void __launch_bounds__(kOrderThreads) count_kernel(const int32_t* ids, int64_t n, int64_t chunk, int E,
+                                                              int32_t* counts) {
+  __shared__ int32_t count[kMaxExperts];
+  wait_for_previous();
+  for (int e = threadIdx.x; e < E; e += kOrderThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t end = min(n, (blockIdx.x + 1) * chunk);
+  for (int64_t i = blockIdx.x * chunk + threadIdx.x; i < end; i += kOrderThreads)
+    if (is_expert(ids[i], E)) atomicAdd(&count[ids[i]], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kOrderThreads) counts[(int64_t)blockIdx.x * E + e] = count[e];
+}
+
+// Rows of the pairs in order of their expert.  One CTA counts for itself (counts NULL); of
+// several, each takes the chunks before its own from count_kernel.  Which row of its expert a pair
+// gets within a chunk is left to the atomics: a row's products do not depend on its place.
+__global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids, int64_t n, int64_t chunk, int E,
+                                                              const int32_t* counts, int32_t* offs, int32_t* row_slot,
+                                                              int32_t* slot_row) {
+  __shared__ int32_t at[kMaxExperts], part[32];
+  wait_for_previous();
+  const int e = threadIdx.x;  // E <= kOrderThreads
+  int total = 0, before = 0;
+  if (counts) {
+    if (e < E) {
+#pragma unroll 8
+      for (int c = 0; c < (int)gridDim.x; ++c) {
+        const int v = counts[(int64_t)c * E + e];
+        total += v;
+        before += c < (int)blockIdx.x ? v : 0;
+      }
+    }
+  } else {
+    if (e < E) at[e] = 0;
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < n; i += kOrderThreads)
+      if (is_expert(ids[i], E)) atomicAdd(&at[ids[i]], 1);
+    __syncthreads();
+    total = e < E ? at[e] : 0;
+  }
+  const int start = exclusive_scan(total, part);
+  if (e < E) {
+    at[e] = start + before;
+    if (blockIdx.x == 0) {
+      offs[e] = start;
+      if (e == E - 1) offs[E] = start + total;
+    }
+  }
+  __syncthreads();
+  const int64_t end = min(n, (blockIdx.x + 1) * chunk);
+  for (int64_t i = blockIdx.x * chunk + threadIdx.x; i < end; i += kOrderThreads) {
     int r = -1;
-    if (e >= 0 && e < E) {
-      r = atomicAdd(&at[e], 1);
+    if (is_expert(ids[i], E)) {
+      r = atomicAdd(&at[ids[i]], 1);
       row_slot[r] = (int32_t)i;
     }
     slot_row[i] = r;
@@ -152,11 +220,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     tc::mbar_fence_init();
   }
-  for (int e = tid; e <= p.E; e += kGemmThreads) offs[e] = p.offs[e];
   if (warp == 1) {
     tc::tmem2_alloc(&bars->tmem_base, 512);
     tc::tmem2_relinquish();
   }
+  wait_for_previous();
+  for (int e = tid; e <= p.E; e += kGemmThreads) offs[e] = p.offs[e];
   if (tid == 0) {
     tc::prefetch_tensormap(&map_w);
     tc::prefetch_tensormap(&map_x);
@@ -302,46 +371,396 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// Rows of x in order of their expert, as bf16.
-__global__ void __launch_bounds__(256) gather_kernel(ExpertArgs a, const int32_t* offs, const int32_t* row_slot,
-                                                     __nv_bfloat16* xp) {
-  const int64_t r = blockIdx.x;
+// Eight e4m3 values and their scale, as the bf16 values that they stand for.
+__device__ __forceinline__ uint4 dequantise(uint2 q, float s) {
+  uint4 o;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((j < 2 ? q.x : q.y) >> (16 * (j & 1)));
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+    w[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return o;
+}
+
+// Rows of x in order of their expert, as bf16: a warp per row, kUnroll 16-byte pieces in flight per
+// lane.
+constexpr int kGatherWarps = 8, kUnroll = 8;
+__global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(ExpertArgs a, const int32_t* offs,
+                                                                  const int32_t* row_slot, __nv_bfloat16* xp) {
+  wait_for_previous();
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * kGatherWarps + (threadIdx.x >> 5);
   if (r >= offs[a.E]) return;
   const int64_t t = row_slot[r] / a.topk;
   uint4* dst = reinterpret_cast<uint4*>(xp + r * a.hidden);
   const int n = a.hidden / 8;
   if (!a.x_scale) {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + t * a.hidden);
-    for (int i = threadIdx.x; i < n; i += 256) dst[i] = src[i];
+    for (int i0 = lane; i0 < n; i0 += 32 * kUnroll) {
+      uint4 v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (i0 + 32 * u < n) v[u] = src[i0 + 32 * u];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (i0 + 32 * u < n) dst[i0 + 32 * u] = v[u];
+    }
     return;
   }
   const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + t * a.hidden);
   const float* sc = a.x_scale + t * ((a.hidden + kScaleGroup - 1) / kScaleGroup);
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const uint2 q = src[i];
-    const float s = sc[i / (kScaleGroup / 8)];
-    uint4 o;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+  for (int i0 = lane; i0 < n; i0 += 32 * kUnroll) {
+    uint2 v[kUnroll];
+    float s[kUnroll];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((j < 2 ? q.x : q.y) >> (16 * (j & 1)));
-      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    dst[i] = o;
+    for (int u = 0; u < kUnroll; ++u)
+      if (i0 + 32 * u < n) {
+        v[u] = src[i0 + 32 * u];
+        s[u] = sc[(i0 + 32 * u) / (kScaleGroup / 8)];
+      }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (i0 + 32 * u < n) dst[i0 + 32 * u] = dequantise(v[u], s[u]);
   }
 }
 
+// out[t] = sum_j weights[t,j] y(t,j) in the order of j: a thread per four channels of a token, the
+// rows of kJ choices in flight.
+constexpr int kJ = 8;
 __global__ void __launch_bounds__(256) combine_kernel(ExpertArgs a, const int32_t* slot_row, const float* yp) {
-  const int64_t t = blockIdx.x;
-  for (int c = threadIdx.x; c < a.hidden; c += 256) {
-    float s = 0.f;
-    for (int j = 0; j < a.topk; ++j) {
-      const int r = slot_row[t * a.topk + j];
-      if (r >= 0) s += a.weights[t * a.topk + j] * yp[(int64_t)r * a.hidden + c];
+  wait_for_previous();
+  const int64_t per = a.hidden / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= per * a.T) return;
+  const int64_t t = i / per;
+  const int c = (int)(i - t * per) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < a.topk; j0 += kJ) {
+    float4 v[kJ];
+    float w[kJ];
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      w[j] = 0.f;
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j0 + j < a.topk) {
+        const int r = slot_row[t * a.topk + j0 + j];
+        if (r >= 0) {
+          w[j] = a.weights[t * a.topk + j0 + j];
+          v[j] = __ldcs(reinterpret_cast<const float4*>(yp + (int64_t)r * a.hidden + c));
+        }
+      }
     }
-    static_cast<__nv_bfloat16*>(a.out)[t * a.hidden + c] = __float2bfloat16_rn(s);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      s.x += w[j] * v[j].x;
+      s.y += w[j] * v[j].y;
+      s.z += w[j] * v[j].z;
+      s.w += w[j] * v[j].w;
+    }
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+  uint2 o;
+  o.x = *reinterpret_cast<const uint32_t*>(&lo);
+  o.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + t * a.hidden + c) = o;
+}
+
+// ---------------------------------------------------------------- few tokens
+//
+// With a handful of pairs the weights of the chosen experts are read once and nothing else counts:
+// matrix-vector products on the CUDA cores, without ordering, gathering and combining.  One CTA
+// per SM takes an even share of the weight rows.  Its producer warp streams them through a ring in
+// shared memory with bulk copies.  A stage is about 32 KB: a turn of the ring costs its threads
+// some 550 clocks, so that stages of 4, 8, 16 and 32 KB stream 2.1, 4.1, 6.9 and 7.0 TB/s (805 MB,
+// nothing else done).  96 KB of ring let the CTAs of both products fit an SM, so that the second
+// one fills its ring while the first one ends.  The eight consumer warps divide a row's channels:
+// each keeps its part of the tokens' rows in registers and reads nothing but weights.  A warp's
+// part of a dot goes to shared memory; every 32 items the warps meet and the parts are summed,
+// always in the same order (meeting at every stage held the stream to 3.6 TB/s).
+constexpr int kFewPairs = 32, kFewTokens = 3, kFewWarps = 8, kFewRows = 2, kFlush = 32;
+constexpr int kFewThreads = (kFewWarps + 1) * 32;
+constexpr uint32_t kFewRing = 96 * 1024;
+constexpr int kFewStages = 8;    // at most
+constexpr int kFewWidth = 8192;  // channels of a row at most
+
+struct FewShared {
+  uint64_t full[kFewStages], empty[kFewStages];
+  float part[2][kFlush][2 * kFewRows][kFewWarps];  // [item][gate, up][pair][warp of the row]
+  float sum[];  // second product: [channels of the CTA][kFewTokens]
+};
+
+// The pairs, one per lane (at most 32): which of them share an expert, and the first of each.
+struct FewPairs {
+  int id;            // this lane's expert, -1: none
+  unsigned same;     // lanes with the same one
+  unsigned leaders;  // first lanes of the experts that are asked for
+  __device__ explicit FewPairs(const ExpertArgs& a) {
+    const int lane = threadIdx.x & 31;
+    id = lane < a.T * a.topk ? a.ids[lane] : -1;
+    if (!is_expert(id, a.E)) id = -1;
+    same = __match_any_sync(0xffffffffu, id);
+    leaders = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
+  }
+};
+
+// How a row's channels and the rows are divided: kP pieces of eight channels per lane, `wide` warps
+// per row, `side` rows at a time, `batch` times in a stage.
+struct FewShape {
+  int wide, side, batch, stages;
+  uint32_t row_bytes, stage_bytes;
+  __device__ FewShape(int K, int P, int rows_per_item, int items) {
+    wide = (K / 8 + 32 * P - 1) / (32 * P);
+    side = kFewWarps / wide;
+    batch = items;
+    row_bytes = (uint32_t)K * 2;
+    stage_bytes = (uint32_t)(batch * side * rows_per_item) * row_bytes;
+    stages = min((int)(kFewRing / stage_bytes), kFewStages);
+  }
+};
+
+__device__ __forceinline__ void unpack(const uint4& v, float* f) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+// The sums over the warp of kV (a power of two) values per lane: value i in lanes
+// i * (32 / kV) .. of the result, with kV - 1 + log2(32 / kV) shuffles.
+template <int kV>
+__device__ __forceinline__ float sum_transposed(float (&v)[kV]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = kV / 2; n >= 1; n >>= 1, o >>= 1) {
+    const bool hi = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float got = __shfl_xor_sync(0xffffffffu, hi ? v[i] : v[i + n], o);
+      v[i] = (hi ? v[i + n] : v[i]) + got;
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (; o >= 1; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
+}
+
+// The i-th set bit of a mask, -1: there are fewer.
+__device__ __forceinline__ int nth_bit(unsigned m, int i) {
+  for (; i > 0; --i) m &= m - 1;
+  return __ffs(m) - 1;
+}
+
+// A role's place in the ring.
+struct FewWalk {
+  int stage = 0;
+  uint32_t phase = 0;
+  int part = 0;  // which half of FewShared::part is next
+  __device__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Turns of a stage: 32 KB of rows of kP * 2048 channels.
+template <bool kUp, int kP>
+constexpr int few_batch() { return (kUp ? 4 : 8) / kP; }
+
+// The items of one expert (`count` weight rows from `row0` on) for all of its pairs, by a consumer
+// warp; kR of the pairs at a time.
+template <bool kUp, int kP, int kR>
+__device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& fs, uint8_t* smem, FewShared* sh, FewWalk& at,
+                                           int row0, int count, unsigned mine, __nv_bfloat16* h, int c0) {
+  constexpr int kNR = kUp ? 2 : 1, kBatch = few_batch<kUp, kP>(), kV = kBatch * kNR * kR, kPer = 32 / kV;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kBatch * kFewWarps <= kFlush && kV <= 32 && 2 * kFewRows >= kNR * kR, "a stage's parts fit FewShared::part");
+  const int kw = warp % fs.wide, g = warp / fs.wide, workers = fs.wide * fs.side * 32;
+  const int K8 = (kUp ? a.hidden : a.inter) / 8, piece = kw * 32 * kP + lane;
+  const int step = kBatch * fs.side, rows = __popc(mine);
+  // the items between two meetings: whole stages, or one stage where it has more
+  const int flush = max(kFlush / step, 1) * step;
+  const int value = lane / kPer;  // this lane's of the kV dots: [turn][gate, up][pair]
+  for (int first = 0; first < rows; first += kR) {
+    // this lane's part of the pairs' rows
+    float x[kR][kP][8];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const int slot = max(nth_bit(mine, first + r), 0);
+#pragma unroll
+      for (int q = 0; q < kP; ++q) {
+        const int i = piece + 32 * q;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < K8) {
+          if (!kUp) {
+            v = reinterpret_cast<const uint4*>(h)[(int64_t)slot * K8 + i];
+          } else {
+            const int64_t t = slot / a.topk;
+            if (a.x_scale)
+              v = dequantise(static_cast<const uint2*>(a.x)[t * K8 + i],
+                             a.x_scale[t * ((a.hidden + kScaleGroup - 1) / kScaleGroup) + i / (kScaleGroup / 8)]);
+            else
+              v = static_cast<const uint4*>(a.x)[t * K8 + i];
+          }
+        }
+        unpack(v, x[r][q]);
+      }
+    }
+    for (int i0 = 0; i0 < count; i0 += flush) {
+      const int n = min(flush, count - i0);
+      float (*part)[2 * kFewRows][kFewWarps] = sh->part[at.part];
+      bool ok = true;
+      for (int i = 0; i < n && ok; i += step) {
+        float acc[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sh->full[at.stage], at.phase, kWaitLimit));
+        const uint8_t* stage = smem + at.stage * fs.stage_bytes;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+          for (int nr = 0; nr < kNR; ++nr) {
+            const uint4* w = reinterpret_cast<const uint4*>(stage + (uint32_t)((nr * kBatch + b) * fs.side + g) * fs.row_bytes);
+#pragma unroll
+            for (int q = 0; q < kP; ++q) {
+              if (piece + 32 * q >= K8 || i + b * fs.side + g >= n) continue;
+              float f[8];
+              unpack(w[piece + 32 * q], f);
+#pragma unroll
+              for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[(b * kNR + nr) * kR + r] = fmaf(f[j], x[r][q][j], acc[(b * kNR + nr) * kR + r]);
+            }
+          }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh->empty[at.stage]);
+        at.next(fs.stages);
+        const float dot = sum_transposed<kV>(acc);
+        if (lane % kPer == 0) part[i + value / (kNR * kR) * fs.side + g][value % (kNR * kR)][kw] = dot;
+      }
+      at.part ^= 1;
+      if (!tc::named_bar_and(1, workers, ok)) return false;
+      // a thread per item; the next write to this half of the parts is behind the next meeting
+      for (int i = warp * 32 + lane; i < n; i += workers) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const int slot = nth_bit(mine, first + r);
+          if (slot < 0) break;
+          float d[kNR];
+#pragma unroll
+          for (int nr = 0; nr < kNR; ++nr) {
+            d[nr] = 0.f;
+            for (int w = 0; w < fs.wide; ++w) d[nr] += part[i][nr * kR + r][w];
+          }
+          if (kUp) {
+            float gate = d[0], u = d[kNR - 1];
+            if (a.limit > 0.f) {
+              gate = gate > a.limit ? a.limit : gate;  // a NaN stays one
+              u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
+            }
+            h[(int64_t)slot * a.inter + row0 + i0 + i] = __float2bfloat16_rn(__fdividef(gate, 1.f + __expf(-gate)) * u);
+          } else {
+            sh->sum[(row0 + i0 + i - c0) * kFewTokens + slot / a.topk] += a.weights[slot] * d[0];
+          }
+        }
+      }
+    }
+  }
+  return true;
+}
+
+template <bool kUp, int kP>
+__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(ExpertArgs a, __nv_bfloat16* h) {
+  constexpr int kNR = kUp ? 2 : 1, kBatch = few_batch<kUp, kP>();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  FewShared* sh = reinterpret_cast<FewShared*>(smem + kFewRing);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const FewShape fs(kUp ? a.hidden : a.inter, kP, kNR, kBatch);
+  // this CTA's share: of the (expert, channel) units in order; of the output channels
+  const int c0 = (int)((int64_t)a.hidden * blockIdx.x / gridDim.x), c1 = (int)((int64_t)a.hidden * (blockIdx.x + 1) / gridDim.x);
+  if (threadIdx.x < fs.stages) {
+    tc::mbar_init(&sh->full[threadIdx.x], 1);
+    tc::mbar_init(&sh->empty[threadIdx.x], fs.wide * fs.side);
+  }
+  if (!kUp)
+    for (int i = threadIdx.x; i < (c1 - c0) * kFewTokens; i += kFewThreads) sh->sum[i] = 0.f;
+  tc::mbar_fence_init();
+  __syncthreads();
+  // The first product waits for what is before the call and only then lets the second one start,
+  // which therefore finds ids, weights and x as they are to be and waits for h alone.
+  if (kUp) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const FewPairs pairs(a);
+  const int64_t units = (int64_t)__popc(pairs.leaders) * a.inter;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const bool producer = warp == kFewWarps;
+  if (!kUp && !producer) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (producer || warp < fs.wide * fs.side) {
+    int64_t base = 0;  // units before the expert
+    FewWalk at;
+    int rounds = 0;    // of the ring, by the producer
+    bool ok = true;
+    for (unsigned left = pairs.leaders; left && ok; left &= left - 1, base += a.inter) {
+      const int leader = __ffs(left) - 1;
+      const int row0 = kUp ? (int)max(u0 - base, (int64_t)0) : c0;
+      const int row1 = kUp ? (int)min(u1 - base, (int64_t)a.inter) : c1;
+      const int count = row1 - row0;
+      if (count <= 0) continue;
+      const int64_t e = __shfl_sync(0xffffffffu, pairs.id, leader);
+      const unsigned mine = __shfl_sync(0xffffffffu, pairs.same, leader);
+      if (producer) {
+        if (lane == 0) {
+          const __nv_bfloat16* w = kUp ? static_cast<const __nv_bfloat16*>(a.w13) + (e * 2 * a.inter + row0) * a.hidden
+                                       : static_cast<const __nv_bfloat16*>(a.w2) + (e * a.hidden + row0) * a.inter;
+          const int64_t K = kUp ? a.hidden : a.inter;
+          const int step = kBatch * fs.side;
+          // once for every kFewRows pairs: the rows of more of them come again
+          for (int pass = 0; pass < __popc(mine) && ok; pass += kFewRows)
+            for (int i = 0; i < count; i += step) {
+              if (rounds > 0 && !tc::mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, kWaitLimit)) {
+                ok = false;
+                break;
+              }
+              const uint32_t bytes = (uint32_t)min(step, count - i) * fs.row_bytes;
+              uint8_t* dst = smem + at.stage * fs.stage_bytes;
+              tc::mbar_arrive_expect_tx(&sh->full[at.stage], kNR * bytes);
+              bulk_load(dst, w + i * K, bytes, &sh->full[at.stage]);
+              if (kUp) bulk_load(dst + step * fs.row_bytes, w + (i + (int64_t)a.inter) * K, bytes, &sh->full[at.stage]);
+              at.next(fs.stages);
+              rounds += at.stage == 0;
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      } else if (__popc(mine) == 1) {
+        ok = few_expert<kUp, kP, 1>(a, fs, smem, sh, at, row0, count, mine, h, c0);
+      } else {
+        ok = few_expert<kUp, kP, kFewRows>(a, fs, smem, sh, at, row0, count, mine, h, c0);
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicExch(&g_experts_error, producer ? 5 : 6);
+      if (producer)  // copies in flight: those of this round, and of the one before it
+        for (int s = 0; s < fs.stages; ++s)
+          if (s < at.stage || rounds > 0) (void)tc::mbar_wait(&sh->full[s], s < at.stage ? at.phase : at.phase ^ 1u, kWaitLimit);
+    }
+  }
+  if (kUp) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < (c1 - c0) * a.T; i += kFewThreads) {
+    const int t = i / (c1 - c0), c = i - t * (c1 - c0);
+    static_cast<__nv_bfloat16*>(a.out)[(int64_t)t * a.hidden + c0 + c] = __float2bfloat16_rn(sh->sum[c * kFewTokens + t]);
   }
 }
 
@@ -379,6 +798,24 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const int64_t* dims, c
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin while the kernel before it in the stream ends (wait_for_previous).
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t grid_x, int grid_y, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid_x, (unsigned)grid_y, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  if (e == cudaSuccess) note_launch(1);
+  return e;
+}
+
 int sm_count() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -414,9 +851,7 @@ cudaError_t launch_gemm(const ExpertArgs& a, const void* rows, int64_t n, const 
   const size_t smem = kSmemTotal + (size_t)(a.E + 1) * 4;
   cudaError_t e = cudaFuncSetAttribute(gemm_kernel<kPass>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  gemm_kernel<kPass><<<sm_count() / 2 * 2, kGemmThreads, smem, st>>>(mw, mx, mx16, p);
-  note_launch(1);
-  return cudaGetLastError();
+  return launch(gemm_kernel<kPass>, sm_count() / 2 * 2, 1, kGemmThreads, smem, st, mw, mx, mx16, p);
 }
 
 }  // namespace
@@ -436,17 +871,36 @@ cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t st) {
   float* yp = reinterpret_cast<float*>(ws + l.yp);
   __nv_bfloat16* xp = reinterpret_cast<__nv_bfloat16*>(yp);  // read before y is written
   const int64_t n = (int64_t)a.T * a.topk;
-  order_kernel<<<1, 1024, 0, st>>>(a.ids, n, a.E, offs, row_slot, slot_row);
-  note_launch(1);
-  gather_kernel<<<(unsigned)n, 256, 0, st>>>(a, offs, row_slot, xp);
-  note_launch(1);
-  cudaError_t e = launch_gemm<0>(a, xp, n, offs, h, st);
+  cudaError_t e;
+  if (n <= kFewPairs && a.T <= kFewTokens && a.hidden <= kFewWidth && a.inter <= kFewWidth) {
+    const int grid = sm_count();
+    const auto up = a.hidden <= kFewWidth / 2 ? few_kernel<true, 2> : few_kernel<true, 4>;
+    const auto down = a.inter <= kFewWidth / 2 ? few_kernel<false, 2> : few_kernel<false, 4>;
+    const size_t up_smem = kFewRing + sizeof(FewShared);
+    const size_t down_smem = up_smem + (size_t)(a.hidden / grid + 1) * kFewTokens * 4;
+    if ((e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)up_smem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)down_smem)) != cudaSuccess) return e;
+    // both CTAs of an SM at once
+    if ((e = cudaFuncSetAttribute(up, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(down, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
+    if ((e = launch(up, grid, 1, kFewThreads, up_smem, st, a, h)) != cudaSuccess) return e;
+    return launch(down, grid, 1, kFewThreads, down_smem, st, a, h);
+  }
+  if (n <= kOneCta) {
+    e = launch(order_kernel, 1, 1, kOrderThreads, 0, st, a.ids, n, n, a.E, nullptr, offs, row_slot, slot_row);
+  } else {
+    const int64_t chunk = (n + kMaxChunks - 1) / kMaxChunks, chunks = (n + chunk - 1) / chunk;
+    int32_t* counts = reinterpret_cast<int32_t*>(ws + l.counts);
+    e = launch(count_kernel, chunks, 1, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts);
+    if (e != cudaSuccess) return e;
+    e = launch(order_kernel, chunks, 1, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts, offs, row_slot, slot_row);
+  }
   if (e != cudaSuccess) return e;
-  e = launch_gemm<1>(a, h, n, offs, yp, st);
+  e = launch(gather_kernel, (n + kGatherWarps - 1) / kGatherWarps, 1, kGatherWarps * 32, 0, st, a, offs, row_slot, xp);
   if (e != cudaSuccess) return e;
-  combine_kernel<<<a.T, 256, 0, st>>>(a, slot_row, yp);
-  note_launch(1);
-  return cudaGetLastError();
+  if ((e = launch_gemm<0>(a, xp, n, offs, h, st)) != cudaSuccess) return e;
+  if ((e = launch_gemm<1>(a, h, n, offs, yp, st)) != cudaSuccess) return e;
+  return launch(combine_kernel, ((int64_t)a.T * (a.hidden / 4) + 255) / 256, 1, 256, 0, st, a, slot_row, yp);
 }
 
 cudaError_t take_experts_error(int* code) {
