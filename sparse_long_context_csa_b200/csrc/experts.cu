@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "moe.h"
 #include "tc_pair.cuh"
 
@@ -35,13 +36,6 @@ Layout layout(int64_t T, int hidden, int inter, int E, int topk) {
   l.yp = l.h + up((size_t)n * inter * 2);
   l.total = l.yp + up((size_t)n * hidden * 4);
   return l;
-}
-
-// A kernel that follows another one in the call waits here for what that one wrote (its launch
-// and its set-up overlap the other's end); the next one may be launched from the start.
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ bool is_expert(int e, int E) { return e >= 0 && e < E; }
@@ -798,24 +792,6 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const int64_t* dims, c
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A launch that may begin while the kernel before it in the stream ends (wait_for_previous).
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int64_t grid_x, int grid_y, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid_x, (unsigned)grid_y, 1);
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-  if (e == cudaSuccess) note_launch(1);
-  return e;
-}
-
 int sm_count() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -851,7 +827,7 @@ cudaError_t launch_gemm(const ExpertArgs& a, const void* rows, int64_t n, const 
   const size_t smem = kSmemTotal + (size_t)(a.E + 1) * 4;
   cudaError_t e = cudaFuncSetAttribute(gemm_kernel<kPass>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch(gemm_kernel<kPass>, sm_count() / 2 * 2, 1, kGemmThreads, smem, st, mw, mx, mx16, p);
+  return launch(gemm_kernel<kPass>, sm_count() / 2 * 2, kGemmThreads, smem, st, mw, mx, mx16, p);
 }
 
 }  // namespace
@@ -883,24 +859,24 @@ cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t st) {
     // both CTAs of an SM at once
     if ((e = cudaFuncSetAttribute(up, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(down, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
-    if ((e = launch(up, grid, 1, kFewThreads, up_smem, st, a, h)) != cudaSuccess) return e;
-    return launch(down, grid, 1, kFewThreads, down_smem, st, a, h);
+    if ((e = launch(up, grid, kFewThreads, up_smem, st, a, h)) != cudaSuccess) return e;
+    return launch(down, grid, kFewThreads, down_smem, st, a, h);
   }
   if (n <= kOneCta) {
-    e = launch(order_kernel, 1, 1, kOrderThreads, 0, st, a.ids, n, n, a.E, nullptr, offs, row_slot, slot_row);
+    e = launch(order_kernel, 1, kOrderThreads, 0, st, a.ids, n, n, a.E, nullptr, offs, row_slot, slot_row);
   } else {
     const int64_t chunk = (n + kMaxChunks - 1) / kMaxChunks, chunks = (n + chunk - 1) / chunk;
     int32_t* counts = reinterpret_cast<int32_t*>(ws + l.counts);
-    e = launch(count_kernel, chunks, 1, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts);
+    e = launch(count_kernel, chunks, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts);
     if (e != cudaSuccess) return e;
-    e = launch(order_kernel, chunks, 1, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts, offs, row_slot, slot_row);
+    e = launch(order_kernel, chunks, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts, offs, row_slot, slot_row);
   }
   if (e != cudaSuccess) return e;
-  e = launch(gather_kernel, (n + kGatherWarps - 1) / kGatherWarps, 1, kGatherWarps * 32, 0, st, a, offs, row_slot, xp);
+  e = launch(gather_kernel, (n + kGatherWarps - 1) / kGatherWarps, kGatherWarps * 32, 0, st, a, offs, row_slot, xp);
   if (e != cudaSuccess) return e;
   if ((e = launch_gemm<0>(a, xp, n, offs, h, st)) != cudaSuccess) return e;
   if ((e = launch_gemm<1>(a, h, n, offs, yp, st)) != cudaSuccess) return e;
-  return launch(combine_kernel, ((int64_t)a.T * (a.hidden / 4) + 255) / 256, 1, 256, 0, st, a, slot_row, yp);
+  return launch(combine_kernel, ((int64_t)a.T * (a.hidden / 4) + 255) / 256, 256, 0, st, a, slot_row, yp);
 }
 
 cudaError_t take_experts_error(int* code) {

@@ -5,9 +5,14 @@
 //   s_g = max_{c in group g} |y_c| / 448,  q_c = e4m3(y_c / s_g)     128 channels per group
 // r is stored as res_out, y as y, (q, s) as yq / yscale; each is rounded once, from the 32-bit
 // value (y is formed from the unrounded r).
+//
+// Bound by memory: every row is read once, kept in registers in 32 bits over the one reduction,
+// and written once.  A lane's pieces are 16 bytes (8 bf16 or 4 fp32 channels), so that the 128
+// channels of a scale lie in 16 or 32 neighbouring lanes.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "moe.h"
 
 namespace dsv4 {
@@ -15,8 +20,8 @@ namespace {
 
 __device__ __forceinline__ float group_scale(float amax, int pow2) {
   float s = amax / kE4M3Max;
-  if (s == 0.f) return 1.f;  // an all-zero group
-  if (pow2 && s < INFINITY) {  // the smallest power of two that is not below it; NaN stays
+  if (s == 0.f) return 1.f;        // an all-zero group
+  if (pow2 && s < INFINITY) {      // the smallest power of two that is not below it; NaN stays
     int e;
     const float m = frexpf(s, &e);
     s = ldexpf(1.f, m == 0.5f ? e - 1 : e);
@@ -24,15 +29,139 @@ __device__ __forceinline__ float group_scale(float amax, int pow2) {
   return s;
 }
 
+// y / s; the reciprocal of a very small scale would leave fp32's range.
+__device__ __forceinline__ float scaled(float y, float s, float inv) { return s >= 0x1p-100f ? y * inv : y / s; }
+
 template <typename T>
-__global__ void __launch_bounds__(256) norm_kernel(NormArgs a) {
+struct Piece;  // 16 bytes of a row
+template <>
+struct Piece<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    uint4 v;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return v;
+  }
+};
+
+// `per` threads (a multiple of 32) have a row, kV pieces each; rows of one warp share a CTA, wider
+// ones have it to themselves.
+template <typename T, int kV>
+__global__ void __launch_bounds__(1024) norm_rows_kernel(NormArgs a, int per) {
+  constexpr int kN = Piece<T>::kN;
+  __shared__ float part[32];
+  const int lane = threadIdx.x & 31, i0 = per == 32 ? lane : threadIdx.x;
+  const int64_t row = per == 32 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const int n = a.hidden / kN;
+  const uint4* w = static_cast<const uint4*>(a.weight);
+  wait_for_previous();
+  if (row >= a.T) return;
+  const uint4* x = static_cast<const uint4*>(a.x) + row * n;
+  const uint4* res = a.residual ? static_cast<const uint4*>(a.residual) + row * n : nullptr;
+  uint4 vx[kV], vr[kV];
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int i = i0 + v * per;
+    vx[v] = vr[v] = make_uint4(0, 0, 0, 0);
+    if (i < n) {
+      vx[v] = x[i];
+      if (res) vr[v] = res[i];
+    }
+  }
+  float r[kV][kN];
+  float sq = 0.f;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    float f[kN];
+    Piece<T>::unpack(vx[v], r[v]);
+    Piece<T>::unpack(vr[v], f);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      r[v][j] += f[j];
+      sq = fmaf(r[v][j], r[v][j], sq);
+    }
+  }
+  if (a.res_out) {
+    uint4* out = static_cast<uint4*>(a.res_out) + row * n;
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      if (i0 + v * per < n) out[i0 + v * per] = Piece<T>::pack(r[v]);
+  }
+  sq = warp_sum(sq);
+  if (per > 32) {
+    if (lane == 0) part[threadIdx.x >> 5] = sq;
+    __syncthreads();
+    sq = warp_sum(lane < (per >> 5) ? part[lane] : 0.f);
+  }
+  const float inv_rms = rsqrtf(sq / (float)a.hidden + a.eps);
+  const int groups = (a.hidden + kScaleGroup - 1) / kScaleGroup;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int i = i0 + v * per;
+    float f[kN];
+    Piece<T>::unpack(i < n ? w[i] : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) r[v][j] = r[v][j] * inv_rms * f[j];
+    if (a.y && i < n) static_cast<uint4*>(a.y)[row * n + i] = Piece<T>::pack(r[v]);
+    if (!a.yq) continue;
+    uint32_t most = 0;  // of the magnitudes' bits: a NaN is above infinity
+#pragma unroll
+    for (int j = 0; j < kN; ++j) most = max(most, __float_as_uint(r[v][j]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = kScaleGroup / kN / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float s = group_scale(__uint_as_float(i < n ? most : 0u), a.scale_pow2), inv = 1.f / s;
+    if (i >= n) continue;
+    if (i % (kScaleGroup / kN) == 0) a.yscale[row * groups + i / (kScaleGroup / kN)] = s;
+    uint32_t q[kN / 4];
+#pragma unroll
+    for (int j = 0; j < kN; j += 4) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(scaled(r[v][j], s, inv), scaled(r[v][j + 1], s, inv)), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(scaled(r[v][j + 2], s, inv), scaled(r[v][j + 3], s, inv)), __NV_SATFINITE, __NV_E4M3);
+      q[j / 4] = lo | (hi << 16);
+    }
+    uint8_t* out = a.yq + (row * n + i) * kN;
+    if (kN == 8)
+      *reinterpret_cast<uint2*>(out) = make_uint2(q[0], q[kN / 4 - 1]);
+    else
+      *reinterpret_cast<uint32_t*>(out) = q[0];
+  }
+}
+
+// Any width: two passes over the row, a warp per group of 128 channels in the second.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   __shared__ float part[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t base = (int64_t)blockIdx.x * a.hidden;
   const T* x = static_cast<const T*>(a.x) + base;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + base : nullptr;
   const T* w = static_cast<const T*>(a.weight);
+  wait_for_previous();
   float sq = 0.f;
+#pragma unroll 4
   for (int c = tid; c < a.hidden; c += 256) {
     const float r = to_f32<T>(x[c]) + (res ? to_f32<T>(res[c]) : 0.f);
     sq += r * r;
@@ -42,44 +171,56 @@ __global__ void __launch_bounds__(256) norm_kernel(NormArgs a) {
   __syncthreads();
   sq = 0.f;
   for (int i = 0; i < 8; ++i) sq += part[i];
-  const float inv = rsqrtf(sq / (float)a.hidden + a.eps);
+  const float inv_rms = rsqrtf(sq / (float)a.hidden + a.eps);
   const int groups = (a.hidden + kScaleGroup - 1) / kScaleGroup;
   for (int g = warp; g < groups; g += 8) {
-    float y[4], amax = 0.f;
-    bool nan = false;
+    float y[4];
+    uint32_t most = 0;  // of the magnitudes' bits: a NaN is above infinity
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = g * kScaleGroup + i * 32 + lane;
       y[i] = 0.f;
       if (c >= a.hidden) continue;
       const float r = to_f32<T>(x[c]) + (res ? to_f32<T>(res[c]) : 0.f);
-      y[i] = r * inv * to_f32<T>(w[c]);
+      y[i] = r * inv_rms * to_f32<T>(w[c]);
       if (a.res_out) static_cast<T*>(a.res_out)[base + c] = from_f32<T>(r);
       if (a.y) static_cast<T*>(a.y)[base + c] = from_f32<T>(y[i]);
-      amax = fmaxf(amax, fabsf(y[i]));
-      nan |= y[i] != y[i];
+      most = max(most, __float_as_uint(y[i]) & 0x7fffffffu);
     }
     if (!a.yq) continue;
-    amax = warp_max(amax);
-    if (__any_sync(0xffffffffu, nan)) amax = nanf("");
-    const float s = group_scale(amax, a.scale_pow2);
+    const float s = group_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, most)), a.scale_pow2), inv = 1.f / s;
     if (lane == 0) a.yscale[(int64_t)blockIdx.x * groups + g] = s;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = g * kScaleGroup + i * 32 + lane;
-      if (c < a.hidden) a.yq[base + c] = __nv_cvt_float_to_fp8(y[i] / s, __NV_SATFINITE, __NV_E4M3);
+      if (c < a.hidden) a.yq[base + c] = __nv_cvt_float_to_fp8(scaled(y[i], s, inv), __NV_SATFINITE, __NV_E4M3);
     }
   }
+}
+
+template <typename T, int kV>
+cudaError_t launch_rows(const NormArgs& a, cudaStream_t st) {
+  const int n = a.hidden / Piece<T>::kN, per = ((n + kV - 1) / kV + 31) / 32 * 32;
+  const int rows = per == 32 ? 8 : 1;  // rows of a CTA
+  return launch(norm_rows_kernel<T, kV>, ((int64_t)a.T + rows - 1) / rows, per * rows, 0, st, a, per);
+}
+
+template <typename T>
+cudaError_t launch_type(const NormArgs& a, cudaStream_t st) {
+  const int n = a.hidden / Piece<T>::kN;
+  if (a.hidden % Piece<T>::kN != 0 || n > 4096) return launch(norm_any_kernel<T>, a.T, 256, 0, st, a);
+  // Many rows: four pieces a thread, which keeps 128 bytes (x and residual) in flight per thread;
+  // few rows: one piece a thread, for the shortest way through the row.
+  if (n > 2048 || (a.T > 512 && n > 32)) return launch_rows<T, 4>(a, st);
+  if (n > 1024) return launch_rows<T, 2>(a, st);
+  return launch_rows<T, 1>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormArgs& a, int dtype, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  if (dtype == DSV4_BF16)
-    norm_kernel<__nv_bfloat16><<<a.T, 256, 0, st>>>(a);
-  else
-    norm_kernel<float><<<a.T, 256, 0, st>>>(a);
-  note_launch(1);
-  return cudaGetLastError();
+  return dtype == DSV4_BF16 ? launch_type<__nv_bfloat16>(a, st) : launch_type<float>(a, st);
 }
 
 }  // namespace dsv4

@@ -1,13 +1,30 @@
 // Routing of tokens to experts: scores from router logits, the choice of topk experts by
 // score + bias within the best groups, and the chosen experts' weights.
+//
+// The order of the choice is that of exact arithmetic.  A warp takes a token and chooses in 32
+// bits: every lane sorts the values of its few experts, then the largest head of the warp's lists
+// is taken topk times.  A value's last bits make room for its place in the lane, so that sorting
+// moves one word per value.  Where two neighbours of the chosen order (or the last group that stays
+// and the first that does not) are closer than what is left and fp32's rounding can tell apart,
+// which for random logits happens to about one token in five hundred, the warp does the token
+// again in 64 bits.  Bound by instruction issue.
 #include "common.cuh"
+#include "launch.cuh"
 #include "moe.h"
 
 namespace dsv4 {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int64_t kBlocks = 148 * 4;  // that an SM of 64 K registers holds at once, for all SMs
+constexpr unsigned kAll = 0xffffffffu;
 
+// Doubles of shared memory per warp: a value per expert, or 32 integers.
+__host__ __device__ constexpr int scratch_of(int E) { return E < 16 ? 16 : E; }
+
+// ---------------------------------------------------------------- 64 bits
+
+// A score is 0 in 64 bits where the logit is below max - 745 (softmax) or -745.
 __device__ __forceinline__ double score64(int fn, double l, double mx, double sum) {
   if (fn == DSV4_SCORE_SOFTMAX) return mx == -INFINITY ? 0.0 : exp(l - mx) / sum;
   if (fn == DSV4_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
@@ -15,43 +32,61 @@ __device__ __forceinline__ double score64(int fn, double l, double mx, double su
 }
 
 __device__ __forceinline__ double warp_sum64(double v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
-// One warp per token; every score in 64 bits.
+// The larger value of the warp, the lower index among equals; index kNone: no value.
+constexpr int kNone = 1 << 30;
+__device__ __forceinline__ void warp_best(double& v, int& at) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double v2 = __shfl_xor_sync(kAll, v, o);
+    const int at2 = __shfl_xor_sync(kAll, at, o);
+    if (at2 != kNone && (at == kNone || v2 > v || (v2 == v && at2 < at))) {
+      v = v2;
+      at = at2;
+    }
+  }
+}
+
+// The chosen experts of one token, lane j the j-th (any E, groups and types); `choice`: E doubles.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
-  extern __shared__ double smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
-  if (t >= a.T) return;
-  double* score = smem + (size_t)warp * 2 * a.E;
-  double* choice = score + a.E;  // NaN: not to be chosen any more
-  const T* row = static_cast<const T*>(a.logits) + t * a.E;
+__device__ __noinline__ int choose64(const RouteArgs& a, const T* row, double* choice) {
+  const int lane = threadIdx.x & 31;
   double mx = -INFINITY, sum = 0.0;
   if (a.score_fn == DSV4_SCORE_SOFTMAX) {
     for (int e = lane; e < a.E; e += 32) mx = fmax(mx, (double)to_f32<T>(row[e]));
-    for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(kAll, mx, o));
     for (int e = lane; e < a.E; e += 32) sum += exp((double)to_f32<T>(row[e]) - mx);
     sum = warp_sum64(sum);
   }
+  __syncwarp();
+  // without a bias the logit chooses, of which every score is a growing function
+  const bool lost = sum != sum && mx != -INFINITY;  // a softmax of a NaN or of +inf: every score is NaN
+  const double floor_l = a.score_fn == DSV4_SCORE_SOFTMAX ? mx - 745.0 : -745.0;
   for (int e = lane; e < a.E; e += 32) {
-    const double s = score64(a.score_fn, (double)to_f32<T>(row[e]), mx, sum);
-    const double c = s + (a.bias ? (double)a.bias[e] : 0.0);
-    score[e] = s;
-    choice[e] = c == c ? c : -INFINITY;
+    const double l = (double)to_f32<T>(row[e]);
+    double c = l < floor_l ? -INFINITY : l;
+    if (a.bias) c = score64(a.score_fn, l, mx, sum) + (double)a.bias[e];
+    choice[e] = c == c && !lost ? c : -INFINITY;
   }
   __syncwarp();
   if (a.n_group > 1) {
     const int per = a.E / a.n_group;
     double best = -INFINITY;
-    bool open = lane < a.n_group;
-    if (open) {
+    if (lane < a.n_group) {
       double b0 = -INFINITY, b1 = -INFINITY;
       for (int i = 0; i < per; ++i) {
         const double c = choice[lane * per + i];
-        if (c > b0) { b1 = b0; b0 = c; } else if (c > b1) { b1 = c; }
+        b1 = c > b0 ? b0 : c > b1 ? c : b1;
+        b0 = c > b0 ? c : b0;
+      }
+      if (!a.bias) {
+        b0 = score64(a.score_fn, b0, mx, sum);
+        b1 = score64(a.score_fn, b1, mx, sum);
       }
       best = per > 1 ? b0 + b1 : b0;
       if (best != best) best = -INFINITY;
@@ -59,61 +94,383 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
     bool kept = false;
     for (int j = 0; j < a.topk_group; ++j) {
       double v = best;
-      int at = open && !kept ? lane : 64;
-      for (int o = 16; o > 0; o >>= 1) {
-        const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
-        const int at2 = __shfl_xor_sync(0xffffffffu, at, o);
-        if (at2 < 64 && (at == 64 || v2 > v || (v2 == v && at2 < at))) { v = v2; at = at2; }
-      }
-      if (at == lane) kept = true;
+      int at = lane < a.n_group && !kept ? lane : kNone;
+      warp_best(v, at);
+      kept |= at == lane;
     }
-    const unsigned kept_mask = __ballot_sync(0xffffffffu, kept);
+    const unsigned kept_mask = __ballot_sync(kAll, kept);
     for (int e = lane; e < a.E; e += 32)
-      if (!((kept_mask >> (e / per)) & 1u)) choice[e] = nan("");
+      if (!((kept_mask >> (e / per)) & 1u)) choice[e] = nan("");  // not to be chosen
     __syncwarp();
   }
-  double mine = 0.0, total = 0.0;
-  int my_id = -1;
+  int mine = 0;
   for (int j = 0; j < a.topk; ++j) {
     double v = 0.0;
-    int at = 1 << 30;
+    int at = kNone;
     for (int e = lane; e < a.E; e += 32) {
       const double c = choice[e];
-      if (c == c && (at == 1 << 30 || c > v)) { v = c; at = e; }
+      if (c == c && (at == kNone || c > v)) {
+        v = c;
+        at = e;
+      }
     }
-    for (int o = 16; o > 0; o >>= 1) {
-      const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
-      const int at2 = __shfl_xor_sync(0xffffffffu, at, o);
-      if (at2 < 1 << 30 && (at == 1 << 30 || v2 > v || (v2 == v && at2 < at))) { v = v2; at = at2; }
-    }
-    const double s = score[at];
-    total += s;
-    if (lane == j) { mine = s; my_id = at; }
+    warp_best(v, at);
+    if (lane == j) mine = at;
     __syncwarp();
     if (lane == 0) choice[at] = nan("");
     __syncwarp();
   }
-  if (lane < a.topk) {
-    a.ids[t * a.topk + lane] = my_id;
-    a.weights[t * a.topk + lane] = (float)((a.renorm ? mine / (total + 1e-20) : mine) * (double)a.routed_scale);
+  return mine;
+}
+
+// The same among `n` <= 31 experts, lane j's e; `at`: 32 integers.
+template <typename T>
+__device__ __noinline__ int choose_of(const RouteArgs& a, const T* row, int e, int n, double mx, int* at) {
+  const int lane = threadIdx.x & 31;
+  double sum = 1.0;
+  if (a.score_fn == DSV4_SCORE_SOFTMAX && a.bias) {
+    sum = 0.0;
+    for (int i = lane; i < a.E; i += 32) sum += exp((double)to_f32<T>(row[i]) - mx);
+    sum = warp_sum64(sum);
   }
+  double c = (double)to_f32<T>(row[e]);
+  if (a.bias)
+    c = score64(a.score_fn, c, mx, sum) + (double)a.bias[e];
+  else if (c < (a.score_fn == DSV4_SCORE_SOFTMAX ? mx - 745.0 : -745.0))
+    c = -INFINITY;
+  if (!(c == c)) c = -INFINITY;
+  int rank = 0;  // of lane's expert
+  for (int j = 0; j < n; ++j) {
+    const double v = __shfl_sync(kAll, c, j);
+    const int f = __shfl_sync(kAll, e, j);
+    rank += v > c || (v == c && f < e);
+  }
+  __syncwarp();
+  if (lane < n) at[rank] = e;
+  __syncwarp();
+  const int mine = lane < n ? at[lane] : 0;
+  __syncwarp();
+  return mine;
+}
+
+// ---------------------------------------------------------------- 32 bits
+
+// Floats as integers in the same order; the lowest is that of -inf, above 0 for every value.
+__device__ __forceinline__ uint32_t order_of(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
+
+// exp(x) and 1 / x to 2 units in the last place, and to 0 where fp32's normal numbers end.
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float score32(int fn, float l, float mx, float inv_sum) {
+  if (fn == DSV4_SCORE_SIGMOID) return rcp_fast(1.f + exp_fast(-l));
+  if (fn == DSV4_SCORE_SOFTMAX) return mx == -INFINITY ? 0.f : exp_fast(l - mx) * inv_sum;
+  return sqrtf(log1pf(expf(-fabsf(l))) + fmaxf(l, 0.f));
+}
+
+// Sorted in descending order (Batcher's odd-even merge sort, kN a power of two).
+template <int kN>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[kN]) {
+#pragma unroll
+  for (int p = 1; p < kN; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j + q < kN; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < kN && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t x = k[i + j], y = k[i + j + q];
+            k[i + j] = max(x, y);
+            k[i + j + q] = min(x, y);
+          }
+}
+
+// The groups that stay, as a mask, in 64 bits; the layout of route_kernel.
+template <typename T>
+__device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int log_lanes, double mx) {
+  const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, per = a.E / a.n_group;
+  const int g = lane >> log_lanes, i = lane & (lanes - 1);
+  double sum = 1.0;
+  if (a.score_fn == DSV4_SCORE_SOFTMAX) {
+    sum = 0.0;
+    for (int e = lane; e < a.E; e += 32) sum += exp((double)to_f32<T>(row[e]) - mx);
+    sum = warp_sum64(sum);
+  }
+  double b0 = -INFINITY, b1 = -INFINITY;
+  for (int j = i; g < a.n_group && j < per; j += lanes) {
+    double c = score64(a.score_fn, (double)to_f32<T>(row[g * per + j]), mx, sum) + (a.bias ? (double)a.bias[g * per + j] : 0.0);
+    c = c == c ? c : -INFINITY;
+    b1 = fmax(b1, fmin(b0, c));
+    b0 = fmax(b0, c);
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    const double m0 = __shfl_xor_sync(kAll, b0, o), m1 = __shfl_xor_sync(kAll, b1, o);
+    b1 = fmax(fmin(b0, m0), fmax(b1, m1));
+    b0 = fmax(b0, m0);
+  }
+  double best = per > 1 ? b0 + b1 : b0;
+  if (best != best) best = -INFINITY;
+  unsigned kept = 0;
+  for (int j = 0; j < a.topk_group; ++j) {
+    double v = best;
+    int at = g < a.n_group && !((kept >> g) & 1u) ? g : kNone;
+    warp_best(v, at);
+    kept |= 1u << at;
+  }
+  return kept;
+}
+
+// A token per warp at a time.  Group g has the kN * lanes slots of `lanes` = 32 / (n_group rounded
+// up to a power of two) neighbouring lanes, its expert j * lanes + i is lane i's j-th.
+// kFull: every lane has kN experts.
+template <typename T, int kN, bool kFull>
+__global__ void __launch_bounds__(kWarps * 32, kN <= 8 ? 4 : kN == 16 ? 2 : 1) route_kernel(RouteArgs a, int log_lanes, int index_bits) {
+  extern __shared__ double smem[];
+  constexpr int kPlace = kN == 1 ? 0 : kN == 2 ? 1 : kN == 4 ? 2 : kN == 8 ? 3 : kN == 16 ? 4 : 5;
+  constexpr float kU = 5.9604645e-8f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lanes = 1 << log_lanes, per = a.E / a.n_group, g = lane >> log_lanes, i = lane & (lanes - 1);
+  const int e0 = g * per + i, count = g < a.n_group ? (per - i + lanes - 1) >> log_lanes : 0;  // this lane's experts
+  const int fn = a.score_fn;
+  // 16-bit logits without a bias are whole in a key's upper half, and the expert's index in the
+  // lower one puts equal ones in order; otherwise a key gives up the bits of the place in the lane.
+  const bool whole = !a.bias && sizeof(T) == 2;
+  const int bits = whole ? index_bits : kPlace;
+  const uint32_t low = (1u << bits) - 1, lowest = order_of(-INFINITY) & ~low;
+  auto value = [&](uint32_t k) { return (k & ~low) == lowest ? -INFINITY : value_of(k & ~low); };
+  const float cut = __int_as_float((127 + bits - 23) << 23);  // what a key leaves out, of the value
+
+  double* scratch = smem + (size_t)warp * scratch_of(a.E);
+  wait_for_previous();
+  int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  float bias[kN], most_bias = 0.f;
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    bias[j] = a.bias && j < count ? a.bias[e0 + j * lanes] : 0.f;
+    if (fabsf(bias[j]) < INFINITY) most_bias = fmaxf(most_bias, fabsf(bias[j]));
+  }
+  if (a.bias) most_bias = warp_max(most_bias);
+  float l[kN];
+  auto load = [&](int64_t token) {
+    const T* p = static_cast<const T*>(a.logits) + token * a.E + e0;
+#pragma unroll
+    for (int j = 0; j < kN; ++j, p += lanes) l[j] = kFull || j < count ? to_f32<T>(*p) : -INFINITY;
+  };
+  if (t < a.T) load(t);
+  for (; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+    float mx = 0.f, sum = 1.f, inv_sum = 1.f;
+    if (fn == DSV4_SCORE_SOFTMAX) {
+      mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) mx = fmaxf(mx, l[j]);
+      mx = warp_max(mx);
+      sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) sum += kFull || j < count ? exp_fast(l[j] - mx) : 0.f;
+      sum = warp_sum(sum);
+      inv_sum = 1.f / sum;
+    }
+    const bool lost = fn == DSV4_SCORE_SOFTMAX && sum != sum && mx != -INFINITY;  // every score is NaN
+    // What is chosen by: score + bias; without a bias the logit, of which every score is a growing
+    // function (all that have a score of 0 in 64 bits are as -inf).
+    if (a.bias) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) l[j] = score32(fn, l[j], mx, inv_sum) + bias[j];
+    } else {
+      const float floor_l = fn == DSV4_SCORE_SOFTMAX ? mx - 745.f : -745.f;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) l[j] = l[j] < floor_l ? -INFINITY : l[j];
+    }
+    if (lost) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) l[j] = -INFINITY;
+    }
+    uint32_t key[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const uint32_t place = whole ? low - (uint32_t)(e0 + j * lanes) : (uint32_t)j;
+      // fmaxf: a NaN is -inf; + 0: -0 is 0
+      key[j] = (order_of(fmaxf(l[j], -INFINITY) + 0.f) & ~low) | place;
+      if (!kFull && j >= count) key[j] = 0u;
+    }
+    const int64_t now = t;
+    if (t + (int64_t)gridDim.x * kWarps < a.T) load(t + (int64_t)gridDim.x * kWarps);  // the next token's
+    sort_down<kN>(key);
+    // fp32's rounding: a score is within 12 u (u = 2^-24) of the largest score + |bias|, its sum with
+    // the bias within one more; the softmax's sum over up to 32 values a lane and 5 steps brings
+    // 50 u.  Without a bias the logits themselves are compared.
+    float blur = 0.f;
+    if (a.bias) {
+      const float top = value(__reduce_max_sync(kAll, key[0]));
+      blur = (fn == DSV4_SCORE_SOFTMAX ? 64.f : 16.f) * kU * (fabsf(top) + 2.f * most_bias);
+    }
+    const T* row = static_cast<const T*>(a.logits) + now * a.E;
+
+    if (a.n_group > a.topk_group) {
+      // the groups' two best, over the group's lanes
+      uint32_t k0 = key[0], k1 = kN > 1 ? key[kN > 1 ? 1 : 0] : 0u;
+      for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t m0 = __shfl_xor_sync(kAll, k0, o), m1 = __shfl_xor_sync(kAll, k1, o);
+        k1 = max(min(k0, m0), max(k1, m1));
+        k0 = max(k0, m0);
+      }
+      float v0 = value(k0), v1 = per > 1 ? value(k1) : 0.f;
+      float off = whole ? 0.f : (fabsf(v0) + fabsf(v1)) * cut;  // the bits that the keys left out
+      if (!a.bias) {  // scores grow by less than the logit does, the softmax's in proportion to itself
+        v0 = score32(fn, v0, mx, inv_sum);
+        v1 = per > 1 ? score32(fn, v1, mx, inv_sum) : 0.f;
+        if (fn == DSV4_SCORE_SOFTMAX) off *= v0 + v1;
+      }
+      off += 2.f * blur + 64.f * kU * (fabsf(v0) + fabsf(v1));
+      float best = v0 + v1;
+      if (!(best == best)) best = -INFINITY;
+      const float worst_off = warp_max(off < INFINITY ? off : 0.f);
+      uint32_t gk = g < a.n_group && i == 0 ? (order_of(best + 0.f) & ~31u) | (31u - (uint32_t)g) : 0u;
+      unsigned kept = 0;
+      uint32_t last = 0;
+      for (int j = 0; j < a.topk_group; ++j) {
+        last = __reduce_max_sync(kAll, gk);
+        if (gk == last) gk = 0u;
+        kept |= 1u << (31u - (last & 31u));
+      }
+      const uint32_t next = __reduce_max_sync(kAll, gk);
+      const float vl = value_of(last & ~31u), vn = value_of(next & ~31u);
+      if (!(vl - vn > 2.f * worst_off + 8e-6f * fabsf(vn)))  // 2^-17: the five bits of the group
+        kept = groups_of<T>(a, row, log_lanes, (double)mx);
+      if (!((kept >> g) & 1u)) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) key[j] = 0u;
+      }
+    }
+
+    // lane j keeps the j-th key and its expert; the one behind the last shows how sure that is
+    uint32_t mine_key = 0u, behind = 0u;
+    int mine = 0;
+    auto take = [&](int j) {
+      const uint32_t best = __reduce_max_sync(kAll, key[0]);
+      const int owner = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+      if (lane == j) {
+        mine_key = best;
+        mine = owner;
+      }
+      if (lane == owner) {
+#pragma unroll
+        for (int v = 0; v + 1 < kN; ++v) key[v] = key[v + 1];
+        key[kN - 1] = 0u;
+      }
+      return best;
+    };
+    for (int j = 0; j <= a.topk; ++j) behind = take(j);
+    auto expert = [&]() {
+      return whole ? (int)(low - (mine_key & low))
+                   : (mine >> log_lanes) * per + (mine & (lanes - 1)) + ((int)(mine_key & low) << log_lanes);
+    };
+    bool doubt = false;
+    if (!whole) {
+      const uint32_t after = __shfl_down_sync(kAll, mine_key, 1), next_key = lane == a.topk - 1 ? behind : after;
+      if (lane < a.topk && next_key != 0u) {
+        const float vp = value(mine_key), vb = value(next_key);
+        doubt = !(vp - vb > fabsf(vb) * cut + 2.f * blur + 1e-37f);
+      }
+      doubt = __any_sync(kAll, doubt);
+    }
+    if (!doubt) {
+      mine = expert();
+    } else {
+      // the order once more in 64 bits, of those that may belong to it: one per lane
+      int n = min(a.topk, 32);
+      const float last = value(__shfl_sync(kAll, mine_key, a.topk - 1)) - 2.f * blur;
+      auto may = [&](uint32_t k) { return k != 0u && !(value(k) + fabsf(value(k)) * cut + 1e-37f < last); };
+      uint32_t k = behind;
+      while (n < 32 && may(k)) k = take(++n);
+      // (lane n's key is the first that does not belong)
+      if (lost || n == 32) {
+        mine = choose64<T>(a, row, scratch);
+      } else {
+        mine = choose_of<T>(a, row, lane < n ? expert() : 0, n, (double)mx, reinterpret_cast<int*>(scratch));
+      }
+    }
+    float s = 0.f;
+    if (lane < a.topk) s = score32(fn, to_f32<T>(row[mine]), mx, inv_sum);
+    if (a.renorm) {
+      const float total = warp_sum(s);
+      s = __fdividef(s, total + 1e-20f);
+    }
+    if (lane < a.topk) {
+      a.ids[now * a.topk + lane] = mine;
+      a.weights[now * a.topk + lane] = s * a.routed_scale;
+    }
+  }
+}
+
+// More experts in a group than 32 registers of its lanes hold: everything in 64 bits.
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) route_wide_kernel(RouteArgs a) {
+  extern __shared__ double smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  wait_for_previous();
+  if (t >= a.T) return;
+  const T* row = static_cast<const T*>(a.logits) + t * a.E;
+  const int mine = choose64<T>(a, row, smem + (size_t)warp * scratch_of(a.E));
+  float mx = -INFINITY, sum = 0.f;
+  if (a.score_fn == DSV4_SCORE_SOFTMAX) {
+    for (int e = lane; e < a.E; e += 32) mx = fmaxf(mx, to_f32<T>(row[e]));
+    mx = warp_max(mx);
+    for (int e = lane; e < a.E; e += 32) sum += exp_fast(to_f32<T>(row[e]) - mx);
+    sum = warp_sum(sum);
+  }
+  float s = 0.f;
+  if (lane < a.topk) s = score32(a.score_fn, to_f32<T>(row[mine]), mx, 1.f / sum);
+  const float total = warp_sum(s);
+  if (lane < a.topk) {
+    a.ids[t * a.topk + lane] = mine;
+    a.weights[t * a.topk + lane] = (a.renorm ? s / (total + 1e-20f) : s) * a.routed_scale;
+  }
+}
+
+template <typename T, int kN>
+void (*pick(const RouteArgs& a))(RouteArgs, int, int) {
+  return a.E == 32 * kN && (a.n_group & (a.n_group - 1)) == 0 ? route_kernel<T, kN, true> : route_kernel<T, kN, false>;
+}
+
+template <typename T>
+cudaError_t launch_type(const RouteArgs& a, cudaStream_t st) {
+  int log_lanes = 5, bits = 0;
+  while ((32 >> log_lanes) < a.n_group) --log_lanes;
+  while ((1 << bits) < a.E) ++bits;
+  const int need = (a.E / a.n_group + (1 << log_lanes) - 1) >> log_lanes;  // experts of a lane
+  const int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
+  const size_t smem = (size_t)kWarps * scratch_of(a.E) * sizeof(double);
+  const auto fn = need <= 1 ? pick<T, 1>(a) : need <= 2 ? pick<T, 2>(a) : need <= 4 ? pick<T, 4>(a) : need <= 8 ? pick<T, 8>(a) :
+                  need <= 16 ? pick<T, 16>(a) : pick<T, 32>(a);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(need <= 32 ? (const void*)fn : (const void*)route_wide_kernel<T>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  if (need > 32) return launch(route_wide_kernel<T>, blocks, kWarps * 32, smem, st, a);
+  return launch(fn, blocks < kBlocks ? blocks : kBlocks, kWarps * 32, smem, st, a, log_lanes, bits);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs& a, int dtype, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  const int grid = (a.T + kWarps - 1) / kWarps;
-  const size_t smem = (size_t)kWarps * 2 * a.E * sizeof(double);
-  const void* fn = dtype == DSV4_BF16 ? (const void*)route_kernel<__nv_bfloat16> : (const void*)route_kernel<float>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  if (dtype == DSV4_BF16)
-    route_kernel<__nv_bfloat16><<<grid, kWarps * 32, smem, st>>>(a);
-  else
-    route_kernel<float><<<grid, kWarps * 32, smem, st>>>(a);
-  note_launch(1);
-  return cudaGetLastError();
+  return dtype == DSV4_BF16 ? launch_type<__nv_bfloat16>(a, st) : launch_type<float>(a, st);
 }
 
 }  // namespace dsv4
