@@ -116,11 +116,42 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> int | None:
+    """The cudaStream_t of a stream; of the current device's current stream when None."""
+    global _raw_stream
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            # the same handle as torch.cuda.current_stream().cuda_stream (3 us) without a Stream object
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+                (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _dense(fn: str, *tensors) -> list:
+    """Pointers of tensors that the kernels can read as the header's shapes say: on the current
+    device (the one that the launch goes to) and contiguous."""
+    import torch
+    current = -1
+    out = []
+    for t in tensors:
+        if t is None or type(t) is int:
+            out.append(t)
+            continue
+        device = t.get_device()
+        if device != current or device < 0:
+            if device >= 0 and current < 0:
+                current = torch.cuda.current_device()
+            if device != current or device < 0:
+                raise Dsv4Error(fn, 1, f"a tensor is on {t.device}, not on the current CUDA device")
+        if not t.is_contiguous():
+            raise Dsv4Error(fn, 1, f"a tensor of strides {tuple(t.stride())} is not contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def _check(fn: str, st: int) -> None:
@@ -226,14 +257,13 @@ def dsv4_grouped_out_proj(params, T, groups, dg, hidden, o, wa, wb, u, y, stream
 def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=None, stream=None):
     """r = x + residual (res_out), y = rms_norm(r) * weight, and y in e4m3 with a scale per 128 channels."""
     _check("dsv4_add_rms_norm", load().dsv4_add_rms_norm(
-        ctypes.byref(params), _ptr(x), _ptr(residual), _ptr(weight), _ptr(res_out), _ptr(y), _ptr(yq), _ptr(yscale),
-        _stream(stream)))
+        ctypes.byref(params), *_dense("dsv4_add_rms_norm", x, residual, weight, res_out, y, yq, yscale), _stream(stream)))
 
 
 def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
     """The topk experts of each token (ids, in descending order of score + bias) and their weights."""
     _check("dsv4_route_experts", load().dsv4_route_experts(
-        ctypes.byref(params), _ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), _stream(stream)))
+        ctypes.byref(params), *_dense("dsv4_route_experts", logits, bias, ids, weights), _stream(stream)))
 
 
 def dsv4_expert_mlp_workspace_bytes(params: Dsv4MoeParams) -> int:
@@ -245,8 +275,8 @@ def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, w
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \
         else (ws_bytes or 0)
     _check("dsv4_expert_mlp", load().dsv4_expert_mlp(
-        ctypes.byref(params), _ptr(x), _ptr(x_scale), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w2), _ptr(out),
-        _ptr(workspace), ws_bytes, _stream(stream)))
+        ctypes.byref(params), *_dense("dsv4_expert_mlp", x, x_scale, ids, weights, w13, w2, out, workspace), ws_bytes,
+        _stream(stream)))
 
 
 def dsv4_set_index_checks(on: bool) -> None:

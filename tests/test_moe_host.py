@@ -114,3 +114,36 @@ def test_binding_raises_with_the_status(abi):
     with pytest.raises(abi.Dsv4Error) as e:
         abi.dsv4_route_experts(_params(abi, topk=0), FAKE, None, FAKE, FAKE, stream=0)
     assert e.value.status == SHAPE
+
+
+def test_binding_refuses_tensors_that_the_kernels_cannot_read(abi, monkeypatch):
+    """A tensor of the host or of another device than the current one, and a strided view, before
+    the library is called."""
+    import torch
+    host = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(abi.Dsv4Error) as e:
+        abi.dsv4_add_rms_norm(_params(abi), host, None, FAKE, None, FAKE, stream=0)
+    assert e.value.status == ARG and "cpu" in str(e.value)
+
+    class Strided:                                                # a device tensor's view, as the binding sees it
+        device = "cuda:0"
+
+        def get_device(self):
+            return 0
+
+        def is_contiguous(self):
+            return False
+
+        def stride(self):
+            return (512, 2)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(abi.Dsv4Error) as e:
+        abi.dsv4_route_experts(_params(abi), Strided(), None, FAKE, FAKE, stream=0)
+    assert e.value.status == ARG and "contiguous" in str(e.value)
+    with pytest.raises(abi.Dsv4Error):
+        abi.dsv4_expert_mlp(_params(abi), FAKE, None, Strided(), FAKE, FAKE, FAKE, FAKE, FAKE, ws_bytes=1, stream=0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(abi.Dsv4Error) as e:                       # on cuda:0 while cuda:1 is current
+        abi.dsv4_route_experts(_params(abi), Strided(), None, FAKE, FAKE, stream=0)
+    assert e.value.status == ARG and "current" in str(e.value)
