@@ -130,7 +130,10 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids
 // One kernel, a CTA pair per 256 x N tile: D[256 weight rows, N token rows] = W X^T, so that the
 // ragged side (the rows of one expert) is N, which an MMA takes in steps of 16, and few rows cost
 // little.  Each CTA of the pair holds 128 weight rows and half of the token rows.
-//  * warp 0: TMA producer, kStages stages of 64 channels (16 KB of weights, up to 16 KB of rows).
+//  * warps 0 and 6: TMA producers of the weights and of the token rows, a ring of stages of 64
+//    channels (16 KB and up to 16 KB).  One thread's turn costs 200 clocks and 150 per load, and a
+//    step of the MMAs takes 512 clocks for 256 rows, 400 for few: so each of the two issues one
+//    load a turn, and a stage's barrier is asked for a step ahead.
 //  * warp 1 (of the leader): M=256, K=16 MMAs into one of two 256-column accumulators, so that
 //    a tile's epilogue overlaps the next tile's main loop.
 //  * warps 2-5: epilogue, one TMEM lane quadrant each.
@@ -140,26 +143,36 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* ids
 // A tile's rows behind its expert's last one are the next expert's (or the fill's): their columns
 // are computed and not stored.  Every wait is bounded; a role that gives up records
 // g_experts_error and leaves, and the others time out behind it.
-constexpr int kBK = 64, kStages = 6, kMaxN = 256;
+constexpr int kBK = 64, kStages = 7, kMaxN = 256;  // kStages: at most
 constexpr uint32_t kStageA = 128 * kBK * 2, kStageB = (kMaxN / 2) * kBK * 2;
-constexpr uint32_t kSmemData = kStages * (kStageA + kStageB);
+
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr int kGemmThreads = 192;
+constexpr int kGemmThreads = 224;
 
 struct GemmParams {
   int N;        // output channels (inter, hidden)
   int K;        // reduction length
   int E;
+  int stages;   // of the ring
   float limit;
   const int32_t* offs;  // [E+1] first row of each expert
   void* out;    // h (bf16) or y (fp32), [rows, N]
+};
+
+// Tensor maps of the token rows in boxes of 16, 32, 64 and 128: a load costs the thread that issues it
+// some 150 clocks whatever its size, so that a tile's rows come in one.
+constexpr int kRowMaps = 4;
+struct RowMaps {
+  CUtensorMap box[kRowMaps];
 };
 
 struct Bars {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   uint32_t tmem_base;
 };
-constexpr uint32_t kSmemTotal = kSmemData + 1024;  // + barriers; the experts' offsets follow
+constexpr uint32_t kSmemMost = 227 * 1024;
+// Stages, then the barriers (1 KB), then the experts' offsets.
+constexpr uint32_t gemm_smem(int stages, int E) { return stages * (kStageA + kStageB) + 1024 + (E + 1) * 4; }
 
 // Walks the tiles of all experts in order: expert, then weight tile, then row tile.
 struct Cursor {
@@ -191,13 +204,14 @@ struct Cursor {
 
 template <int kPass>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                const __grid_constant__ CUtensorMap map_x16, const __grid_constant__ GemmParams p) {
+    gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps maps,
+                const __grid_constant__ GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = tc::cluster_cta_rank();
-  Bars* bars = reinterpret_cast<Bars*>(smem + kSmemData);
-  int32_t* offs = reinterpret_cast<int32_t*>(smem + kSmemTotal);
+  const int stages = p.stages;
+  Bars* bars = reinterpret_cast<Bars*>(smem + stages * (kStageA + kStageB));
+  int32_t* offs = reinterpret_cast<int32_t*>(smem + stages * (kStageA + kStageB) + 1024);
   const int k_steps = (p.K + kBK - 1) / kBK;
   const int weight_tiles = kPass == 0 ? (p.N + 127) / 128 : (p.N + 255) / 256;
   const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
@@ -222,8 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   for (int e = tid; e <= p.E; e += kGemmThreads) offs[e] = p.offs[e];
   if (tid == 0) {
     tc::prefetch_tensormap(&map_w);
-    tc::prefetch_tensormap(&map_x);
-    tc::prefetch_tensormap(&map_x16);
+    for (int i = 0; i < kRowMaps; ++i) tc::prefetch_tensormap(&maps.box[i]);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -233,48 +246,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   if (!aligned) {
     if (tid == 0) atomicExch(&g_experts_error, 3);
-  } else if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
+  } else if (warp == 0 || warp == 6) {
+    // ------------------------------------------------------------------ TMA producers
     if (lane == 0) {
+      const bool weights = warp == 0;
       Cursor cur(offs, p.E, weight_tiles);
-      uint32_t it = 0;
-      bool ok = true;
+      int s = 0;
+      uint32_t phase = 1;            // the first round finds every stage free
+      bool ok = true, free = false;  // free: stage s is known to be
+      bool first = true;
+      const uint32_t full0 = tc::cluster_addr(&bars->full[0], 0);
       int w, row, rows;
       for (int64_t t = pair; ok && cur.at(t, &w, &row, &rows); t += pairs) {
         const int half = (rows + 15) / 16 * 8;  // token rows of one CTA
         const int y = row + (int)rank * half;
-        const int boxes = half > 64 ? 0 : (half + 15) / 16;  // one box of 128 rows, or boxes of 16
-        const uint32_t bytes = kStageA + (boxes ? boxes * 16u : 128u) * kBK * 2;
-        for (int k = 0; k < k_steps; ++k, ++it) {
-          const int s = (int)(it % kStages);
-          if (it >= kStages && !tc::mbar_wait(&bars->empty[s], ((it / kStages) - 1) & 1, kWaitLimit)) {
+        const int size = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;  // one box of 16 << size rows
+        const CUtensorMap* map = &maps.box[size];
+        const uint32_t bytes = 2 * (kStageA + (16u << size) * kBK * 2);
+        const int y_w = kPass == 0 ? w * 8 + (int)rank * 4 : w * 256 + (int)rank * 128;
+        for (int k = 0; k < k_steps; ++k) {
+          if (!free && !first && !tc::mbar_wait(&bars->empty[s], phase, kWaitLimit)) {
             ok = false;
             break;
           }
           uint8_t* sa = smem + s * (kStageA + kStageB);
-          const uint32_t full = tc::cluster_addr(&bars->full[s], 0);
-          if (rank == 0) tc::mbar_arrive_expect_tx(&bars->full[s], 2 * bytes);
-          if (kPass == 0)
-            tc::tma2_load_5d(sa, &map_w, k * kBK, 0, 0, w * 8 + (int)rank * 4, cur.e, full);
-          else
-            tc::tma2_load_3d(sa, &map_w, k * kBK, w * 256 + (int)rank * 128, cur.e, full);
-          if (boxes == 0) tc::tma2_load_2d(sa + kStageA, &map_x, k * kBK, y, full);
-          for (int b = 0; b < boxes; ++b)
-            tc::tma2_load_2d(sa + kStageA + b * 16 * kBK * 2, &map_x16, k * kBK, y + 16 * b, full);
+          uint64_t* here = &bars->full[s];
+          const uint32_t full = full0 + s * 8;
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+            first = false;
+          }
+          if (weights) {
+            if (rank == 0) tc::mbar_arrive_expect_tx(here, bytes);
+            free = kPass == 0 ? tc::tma2_load_5d_test(sa, &map_w, k * kBK, 0, 0, y_w, cur.e, full, &bars->empty[s], phase)
+                              : tc::tma2_load_3d_test(sa, &map_w, k * kBK, y_w, cur.e, full, &bars->empty[s], phase);
+          } else {
+            free = tc::tma2_load_2d_test(sa + kStageA, map, k * kBK, y, full, &bars->empty[s], phase);
+          }
         }
       }
       if (!ok) {
         atomicExch(&g_experts_error, 1);
-        for (uint32_t i = it < kStages ? 0 : it - kStages; rank == 0 && i < it; ++i)  // copies in flight
-          (void)tc::mbar_wait(&bars->full[i % kStages], (i / kStages) & 1, kWaitLimit);
+        // copies in flight: those of this round, and of the one before it (a stage's full phase of a
+        // round is the one that `phase` was not)
+        for (int i = 0; i < stages && rank == 0; ++i)
+          if (i < s || !first) (void)tc::mbar_wait(&bars->full[i], i < s ? phase ^ 1u : phase, kWaitLimit);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer (the leader's)
     if (rank == 0 && lane == 0) {
       Cursor cur(offs, p.E, weight_tiles);
-      uint32_t it = 0, lt = 0;
-      bool ok = true;
+      int s = 0;
+      uint32_t phase = 0, lt = 0;
+      bool ok = true, full = false;  // full: stage s is known to be
+      const uint32_t smem0 = tc::smem_u32(smem);
       int w, row, rows;
       for (int64_t t = pair; ok && cur.at(t, &w, &row, &rows); t += pairs, ++lt) {
         const int buf = (int)(lt & 1);
@@ -285,19 +312,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         tc::tc_fence_after();
         const uint32_t idesc = tc::idesc_bf16_f32(256, (rows + 15) / 16 * 16, 0, 0);
         const uint32_t acc = tmem + buf * kMaxN;
-        for (int k = 0; k < k_steps; ++k, ++it) {
-          const int s = (int)(it % kStages);
-          if (!tc::mbar_wait(&bars->full[s], (it / kStages) & 1, kWaitLimit)) {
+        for (int k = 0; k < k_steps; ++k) {
+          if (!full && !tc::mbar_wait(&bars->full[s], phase, kWaitLimit)) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
-          const uint32_t a0 = tc::smem_u32(smem + s * (kStageA + kStageB));
-          const uint64_t ad = tc::sdesc_sw128(a0, 16, 1024), bd = tc::sdesc_sw128(a0 + kStageA, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc::umma2_f16(acc, ad + 2 * kk, bd + 2 * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
-          tc::umma2_commit_both(&bars->empty[s]);  // free in both CTAs once these MMAs have read it
+          const uint32_t a0 = smem0 + s * (kStageA + kStageB);
+          uint64_t* done = &bars->empty[s];  // free in both CTAs once these MMAs have read it
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+          full = tc::umma2_f16_step(acc, tc::sdesc_sw128(a0, 16, 1024), tc::sdesc_sw128(a0 + kStageA, 16, 1024), idesc,
+                                    k > 0 ? 1u : 0u, done, &bars->full[s], phase);
         }
         if (ok) tc::umma2_commit_both(&bars->acc_full[buf]);
       }
@@ -808,7 +836,8 @@ cudaError_t launch_gemm(const ExpertArgs& a, const void* rows, int64_t n, const 
   p.limit = a.limit;
   p.offs = offs;
   p.out = out;
-  CUtensorMap mw, mx, mx16;
+  CUtensorMap mw;
+  RowMaps maps;
   bool ok;
   if (kPass == 0) {  // [E, 2, inter/16, 16, hidden] read as boxes of 16 gate rows, 16 up rows, four times
     const int64_t d[5] = {p.K, 16, 2, a.inter / 16, a.E};
@@ -821,13 +850,16 @@ cudaError_t launch_gemm(const ExpertArgs& a, const void* rows, int64_t n, const 
     ok = make_map(&mw, a.w2, 3, d, s, b);
   }
   const int64_t d[2] = {p.K, n}, s[1] = {p.K};
-  const int b[2] = {kBK, kMaxN / 2}, b16[2] = {kBK, 16};
-  ok = ok && make_map(&mx, rows, 2, d, s, b) && make_map(&mx16, rows, 2, d, s, b16);
+  for (int i = 0; i < kRowMaps; ++i) {
+    const int b[2] = {kBK, 16 << i};
+    ok = ok && make_map(&maps.box[i], rows, 2, d, s, b);
+  }
   if (!ok) return cudaErrorInvalidValue;
-  const size_t smem = kSmemTotal + (size_t)(a.E + 1) * 4;
+  p.stages = gemm_smem(kStages, a.E) <= kSmemMost ? kStages : kStages - 1;  // 7 of up to 511 experts
+  const size_t smem = gemm_smem(p.stages, a.E);
   cudaError_t e = cudaFuncSetAttribute(gemm_kernel<kPass>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch(gemm_kernel<kPass>, sm_count() / 2 * 2, kGemmThreads, smem, st, mw, mx, mx16, p);
+  return launch(gemm_kernel<kPass>, sm_count() / 2 * 2, kGemmThreads, smem, st, mw, maps, p);
 }
 
 }  // namespace

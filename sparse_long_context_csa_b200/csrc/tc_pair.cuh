@@ -51,6 +51,51 @@ __device__ __forceinline__ void tma2_load_5d(void* dst, const CUtensorMap* map, 
       : "memory");
 }
 
+// The same, and whether the phase of `next` is complete: asked for ahead of the load and looked at
+// behind it.
+__device__ __forceinline__ bool tma2_load_2d_test(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                                  uint64_t* next, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%6], %7;\n\t"
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%3, %4}], [%5];\n\t"
+      "selp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(smem_u32(next)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool tma2_load_3d_test(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                                  uint64_t* next, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%7], %8;\n\t"
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%3, %4, %5}], [%6];\n\t"
+      "selp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(smem_u32(next)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool tma2_load_5d_test(void* dst, const CUtensorMap* map, int x, int y, int z, int v, int w, uint32_t bar,
+                                                  uint64_t* next, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%9], %10;\n\t"
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%3, %4, %5, %6, %7}], [%8];\n\t"
+      "selp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w), "r"(bar), "r"(smem_u32(next)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Whole-warp operations, by one warp of each CTA of the pair.
 __device__ __forceinline__ void tmem2_alloc(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
@@ -82,6 +127,34 @@ __device__ __forceinline__ void umma2_commit_both(uint64_t* bar) {
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+
+// Four such steps of 16 channels over 64, operands in 128-byte rows, and the commit of them on the
+// barrier at `done`'s offset in both CTAs.  Returns whether the phase of `next` is complete; it is
+// asked for ahead of the MMAs and looked at behind them (the answer takes 180 clocks, issuing them
+// 340).
+__device__ __forceinline__ bool umma2_f16_step(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate, uint64_t* done, uint64_t* next, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, r, t;\n\t.reg .b64 a, b;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%8], %9;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%1], %2, %3, %4, p;\n\t"
+      "add.s64 a, %2, 2;\n\tadd.s64 b, %3, 2;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%1], a, b, %4, t;\n\t"
+      "add.s64 a, %2, 4;\n\tadd.s64 b, %3, 4;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%1], a, b, %4, t;\n\t"
+      "add.s64 a, %2, 6;\n\tadd.s64 b, %3, 6;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%1], a, b, %4, t;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], %7;\n\t"
+      "selp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(ok)
+      : "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(smem_u32(done)), "h"((uint16_t)3),
+        "r"(smem_u32(next)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 }  // namespace tc
