@@ -150,52 +150,96 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormArgs a, int per) {
   }
 }
 
-// Any width: two passes over the row, a warp per group of 128 channels in the second.
-template <typename T>
+// Any width, element by element: a warp has whole groups of 128 channels, four per lane.  kG > 0: at
+// most kG groups per warp, kept in registers over the reduction; 0: the row is read a second time.
+// kW of a CTA's eight warps have a row.
+template <typename T, int kG, int kW>
 __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   __shared__ float part[8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t base = (int64_t)blockIdx.x * a.hidden;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp % kW;
+  const int64_t asked = (int64_t)blockIdx.x * (8 / kW) + warp / kW;
+  const bool live = asked < a.T;  // a warp without a row goes along with the last one's, for the barrier
+  const int64_t row = live ? asked : a.T - 1, base = row * a.hidden;
   const T* x = static_cast<const T*>(a.x) + base;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + base : nullptr;
   const T* w = static_cast<const T*>(a.weight);
   wait_for_previous();
-  float sq = 0.f;
-#pragma unroll 4
-  for (int c = tid; c < a.hidden; c += 256) {
-    const float r = to_f32<T>(x[c]) + (res ? to_f32<T>(res[c]) : 0.f);
-    sq += r * r;
+  const int groups = (a.hidden + kScaleGroup - 1) / kScaleGroup;
+  auto load = [&](int g, float* r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = g * kScaleGroup + i * 32 + lane;
+      r[i] = 0.f;
+      if (c < a.hidden) r[i] = to_f32<T>(x[c]) + (res ? to_f32<T>(res[c]) : 0.f);
+    }
+  };
+  constexpr int kHeld = kG > 0 ? kG : 1;
+  float r[kHeld][4], sq = 0.f;
+  if (kG > 0) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) load(w0 + k * kW, r[k]);  // zero past the row
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sq = fmaf(r[k][i], r[k][i], sq);
+  } else {
+#pragma unroll 2
+    for (int g = w0; g < groups; g += kW) {
+      load(g, r[0]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sq = fmaf(r[0][i], r[0][i], sq);
+    }
   }
   sq = warp_sum(sq);
-  if (lane == 0) part[warp] = sq;
-  __syncthreads();
-  sq = 0.f;
-  for (int i = 0; i < 8; ++i) sq += part[i];
+  if (kW > 1) {
+    if (lane == 0) part[warp] = sq;
+    __syncthreads();
+    sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) sq += part[warp - w0 + i];
+  }
+  if (!live) return;
   const float inv_rms = rsqrtf(sq / (float)a.hidden + a.eps);
-  const int groups = (a.hidden + kScaleGroup - 1) / kScaleGroup;
-  for (int g = warp; g < groups; g += 8) {
-    float y[4];
+  auto finish = [&](int g, float* v) {
     uint32_t most = 0;  // of the magnitudes' bits: a NaN is above infinity
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = g * kScaleGroup + i * 32 + lane;
-      y[i] = 0.f;
       if (c >= a.hidden) continue;
-      const float r = to_f32<T>(x[c]) + (res ? to_f32<T>(res[c]) : 0.f);
-      y[i] = r * inv_rms * to_f32<T>(w[c]);
-      if (a.res_out) static_cast<T*>(a.res_out)[base + c] = from_f32<T>(r);
-      if (a.y) static_cast<T*>(a.y)[base + c] = from_f32<T>(y[i]);
-      most = max(most, __float_as_uint(y[i]) & 0x7fffffffu);
+      if (a.res_out) static_cast<T*>(a.res_out)[base + c] = from_f32<T>(v[i]);
+      v[i] = v[i] * inv_rms * to_f32<T>(w[c]);
+      if (a.y) static_cast<T*>(a.y)[base + c] = from_f32<T>(v[i]);
+      most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
     }
-    if (!a.yq) continue;
+    if (!a.yq) return;
     const float s = group_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, most)), a.scale_pow2), inv = 1.f / s;
-    if (lane == 0) a.yscale[(int64_t)blockIdx.x * groups + g] = s;
+    if (lane == 0) a.yscale[row * groups + g] = s;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = g * kScaleGroup + i * 32 + lane;
-      if (c < a.hidden) a.yq[base + c] = __nv_cvt_float_to_fp8(scaled(y[i], s, inv), __NV_SATFINITE, __NV_E4M3);
+      if (c < a.hidden) a.yq[base + c] = __nv_cvt_float_to_fp8(scaled(v[i], s, inv), __NV_SATFINITE, __NV_E4M3);
+    }
+  };
+  if (kG > 0) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (w0 + k * kW < groups) finish(w0 + k * kW, r[k]);
+  } else {
+    for (int g = w0; g < groups; g += kW) {
+      load(g, r[0]);
+      finish(g, r[0]);
     }
   }
+}
+
+template <typename T>
+cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
+  // Up to 2048 channels the row stays in registers (16384 x 333 bf16: 15.4 us, 29.6 in two passes of a
+  // CTA per row; 3001 x 1111 fp32: 8.1 and 8.6 us).
+  if (a.hidden <= 4 * kScaleGroup) return launch(norm_any_kernel<T, 4, 1>, ((int64_t)a.T + 7) / 8, 256, 0, st, a);
+  if (a.hidden <= 8 * kScaleGroup) return launch(norm_any_kernel<T, 4, 2>, ((int64_t)a.T + 3) / 4, 256, 0, st, a);
+  if (a.hidden <= 16 * kScaleGroup) return launch(norm_any_kernel<T, 2, 8>, a.T, 256, 0, st, a);
+  return launch(norm_any_kernel<T, 0, 8>, a.T, 256, 0, st, a);
 }
 
 template <typename T, int kV>
@@ -208,7 +252,7 @@ cudaError_t launch_rows(const NormArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_type(const NormArgs& a, cudaStream_t st) {
   const int n = a.hidden / Piece<T>::kN;
-  if (a.hidden % Piece<T>::kN != 0 || n > 4096) return launch(norm_any_kernel<T>, a.T, 256, 0, st, a);
+  if (a.hidden % Piece<T>::kN != 0 || n > 4096) return launch_any<T>(a, st);
   // Many rows: four pieces a thread, which keeps 128 bytes (x and residual) in flight per thread;
   // few rows: one piece a thread, for the shortest way through the row.
   if (n > 2048 || (a.T > 512 && n > 32)) return launch_rows<T, 4>(a, st);

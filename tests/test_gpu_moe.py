@@ -86,7 +86,8 @@ def check_norm(x, residual, weight, eps, res_out, y, q, s, pow2):
 
 
 NORM_SHAPES = [(1, 4096), (3, 1), (5, 7), (2, 31), (4, 128), (7, 129), (9, 1111), (2, 640), (33, 2048), (17, 8192), (130, 512),
-               (2, 8200), (1, 16384), (3, 20001), (1000, 72)]
+               (2, 8200), (1, 16384), (3, 20001), (1000, 72), (21, 333), (9, 700), (5, 2047), (6, 2049), (600, 256), (3, 32768),
+               (2, 40000)]
 
 
 @pytest.mark.parametrize("T,hidden", NORM_SHAPES)
@@ -170,7 +171,7 @@ def check_route(abi, logits, bias, fn, topk, n_group=1, topk_group=1, renorm=1, 
 
 ROUTES = [  # T, E, topk, n_group, topk_group
     (1, 1, 1, 1, 1), (3, 2, 2, 1, 1), (65, 8, 3, 1, 1), (64, 256, 6, 1, 1), (129, 256, 8, 8, 4), (33, 60, 4, 1, 1),
-    (50, 96, 5, 3, 2), (31, 512, 12, 8, 3), (17, 1024, 32, 32, 32), (9, 33, 32, 1, 1), (20, 32, 4, 32, 7), (40, 14, 7, 2, 1),
+    (50, 96, 5, 3, 2), (12, 1023, 8, 3, 2), (5000, 64, 6, 8, 3), (31, 512, 12, 8, 3), (17, 1024, 32, 32, 32), (9, 33, 32, 1, 1), (20, 32, 4, 32, 7), (40, 14, 7, 2, 1),
     (700, 400, 10, 1, 1)]
 
 
@@ -322,7 +323,10 @@ EXPERTS = [  # T, hidden, inter, E, topk
     (1, 16, 16, 1, 1), (1, 256, 128, 8, 2), (1, 4096, 2048, 8, 6), (2, 144, 80, 5, 3), (3, 1040, 272, 16, 4), (5, 512, 256, 64, 6),
     (8, 2048, 512, 4, 2), (17, 128, 1040, 3, 2), (31, 272, 48, 128, 8), (64, 1024, 512, 16, 4), (65, 96, 112, 2, 1),
     (100, 640, 384, 1, 1), (129, 512, 144, 7, 3), (257, 384, 256, 4, 2), (300, 1024, 768, 64, 6), (777, 256, 128, 1000, 5),
-    (1000, 528, 304, 8, 4), (2049, 512, 512, 16, 2)]
+    (1000, 528, 304, 8, 4), (2049, 512, 512, 16, 2),
+    (2, 4112, 4112, 3, 2), (3, 8192, 272, 4, 3), (1, 8208, 64, 3, 2), (2, 64, 8208, 3, 2),  # widths at the few-token path's ends
+    (3, 512, 256, 2, 2), (4, 512, 256, 2, 2), (3, 16, 16, 2, 11), (1, 48, 16, 40, 33),      # tokens and pairs at its ends
+    (272, 256, 128, 1, 1), (511, 128, 64, 1, 1), (600, 192, 80, 511, 7), (600, 192, 80, 512, 7), (1025, 128, 32, 1, 4)]
 
 
 @pytest.mark.parametrize("T,hidden,inter,E,topk", EXPERTS)
