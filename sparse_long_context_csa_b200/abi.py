@@ -116,41 +116,48 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-_raw_stream = None
+_torch_now = None
+
+
+def _now():
+    """(the current CUDA device, its current stream's cudaStream_t): what torch.cuda.current_device()
+    and current_stream().cuda_stream say, without a Stream object (3 us)."""
+    global _torch_now
+    if _torch_now is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA
+        _torch_now = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                      getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream))
+    device = _torch_now[0]()
+    return device, _torch_now[1](device)
 
 
 def _stream(stream) -> int | None:
-    """The cudaStream_t of a stream; of the current device's current stream when None."""
-    global _raw_stream
     if stream is None:
-        import torch
-        if _raw_stream is None:
-            # the same handle as torch.cuda.current_stream().cuda_stream (3 us) without a Stream object
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-                (lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        return _now()[1]
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _dense(fn: str, *tensors) -> list:
-    """Pointers of tensors that the kernels can read as the header's shapes say: on the current
-    device (the one that the launch goes to) and contiguous."""
-    import torch
-    current = -1
-    out = []
-    for t in tensors:
-        if t is None or type(t) is int:
-            out.append(t)
-            continue
-        device = t.get_device()
-        if device != current or device < 0:
-            if device >= 0 and current < 0:
-                current = torch.cuda.current_device()
-            if device != current or device < 0:
-                raise Dsv4Error(fn, 1, f"a tensor is on {t.device}, not on the current CUDA device")
-        if not t.is_contiguous():
-            raise Dsv4Error(fn, 1, f"a tensor of strides {tuple(t.stride())} is not contiguous")
-        out.append(t.data_ptr())
+def _refuse(fn: str, t, device: int):
+    if t.get_device() != device:
+        raise Dsv4Error(fn, 1, f"a tensor is on {t.device}, not on the current CUDA device")
+    raise Dsv4Error(fn, 1, f"a tensor of strides {tuple(t.stride())} is not contiguous")
+
+
+def _dense(fn: str, stream, *tensors) -> list:
+    """Pointers of tensors that the kernels can read as the header's shapes say, on the current device
+    (the one that the launch goes to) and contiguous; then the stream's handle."""
+    first = tensors[0]
+    if first is None or type(first) is int:  # raw pointers: as the C call takes them
+        first = next((t for t in tensors if t is not None and type(t) is not int), None)
+        if first is None:
+            return [*tensors, _stream(stream)]
+    if first.get_device() < 0:
+        _refuse(fn, first, 0)
+    device, current = _now()
+    out = [t if t is None or type(t) is int else
+           t.data_ptr() if t.get_device() == device and t.is_contiguous() else _refuse(fn, t, device) for t in tensors]
+    out.append(current if stream is None else _stream(stream))
     return out
 
 
@@ -257,13 +264,13 @@ def dsv4_grouped_out_proj(params, T, groups, dg, hidden, o, wa, wb, u, y, stream
 def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=None, stream=None):
     """r = x + residual (res_out), y = rms_norm(r) * weight, and y in e4m3 with a scale per 128 channels."""
     _check("dsv4_add_rms_norm", load().dsv4_add_rms_norm(
-        ctypes.byref(params), *_dense("dsv4_add_rms_norm", x, residual, weight, res_out, y, yq, yscale), _stream(stream)))
+        ctypes.byref(params), *_dense("dsv4_add_rms_norm", stream, x, residual, weight, res_out, y, yq, yscale)))
 
 
 def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
     """The topk experts of each token (ids, in descending order of score + bias) and their weights."""
     _check("dsv4_route_experts", load().dsv4_route_experts(
-        ctypes.byref(params), *_dense("dsv4_route_experts", logits, bias, ids, weights), _stream(stream)))
+        ctypes.byref(params), *_dense("dsv4_route_experts", stream, logits, bias, ids, weights)))
 
 
 def dsv4_expert_mlp_workspace_bytes(params: Dsv4MoeParams) -> int:
@@ -274,9 +281,8 @@ def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, w
     """The weighted sum of each token's experts' clamped SwiGLU products."""
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \
         else (ws_bytes or 0)
-    _check("dsv4_expert_mlp", load().dsv4_expert_mlp(
-        ctypes.byref(params), *_dense("dsv4_expert_mlp", x, x_scale, ids, weights, w13, w2, out, workspace), ws_bytes,
-        _stream(stream)))
+    *ptrs, stream = _dense("dsv4_expert_mlp", stream, x, x_scale, ids, weights, w13, w2, out, workspace)
+    _check("dsv4_expert_mlp", load().dsv4_expert_mlp(ctypes.byref(params), *ptrs, ws_bytes, stream))
 
 
 def dsv4_set_index_checks(on: bool) -> None:

@@ -137,13 +137,13 @@ def test_binding_refuses_tensors_that_the_kernels_cannot_read(abi, monkeypatch):
         def stride(self):
             return (512, 2)
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(abi, "_now", lambda: (0, 0))
     with pytest.raises(abi.Dsv4Error) as e:
         abi.dsv4_route_experts(_params(abi), Strided(), None, FAKE, FAKE, stream=0)
     assert e.value.status == ARG and "contiguous" in str(e.value)
     with pytest.raises(abi.Dsv4Error):
         abi.dsv4_expert_mlp(_params(abi), FAKE, None, Strided(), FAKE, FAKE, FAKE, FAKE, FAKE, ws_bytes=1, stream=0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(abi, "_now", lambda: (1, 0))
     with pytest.raises(abi.Dsv4Error) as e:                       # on cuda:0 while cuda:1 is current
         abi.dsv4_route_experts(_params(abi), Strided(), None, FAKE, FAKE, stream=0)
     assert e.value.status == ARG and "current" in str(e.value)
