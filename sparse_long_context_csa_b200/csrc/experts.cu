@@ -817,13 +817,6 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const int64_t* dims, c
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
-}
-
 template <int kPass>
 cudaError_t launch_gemm(const ExpertArgs& a, const void* rows, int64_t n, const int32_t* offs, void* out, cudaStream_t st) {
   GemmParams p{};

@@ -16,6 +16,13 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+inline int sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 148;
+}
+
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg{};

@@ -16,7 +16,8 @@ namespace dsv4 {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int64_t kBlocks = 148 * 4;  // that an SM of 64 K registers holds at once, for all SMs
+// CTAs of a kernel with kN experts a lane that an SM holds at once (its registers).
+constexpr int ctas_of(int kN) { return kN <= 4 ? 4 : kN == 8 ? 3 : kN == 16 ? 2 : 1; }
 constexpr unsigned kAll = 0xffffffffu;
 
 // Doubles of shared memory per warp: a value per expert, or 32 integers.
@@ -174,10 +175,19 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// fn: known at compile time where it matters.
 __device__ __forceinline__ float score32(int fn, float l, float mx, float inv_sum) {
   if (fn == DSV4_SCORE_SIGMOID) return rcp_fast(1.f + exp_fast(-l));
   if (fn == DSV4_SCORE_SOFTMAX) return mx == -INFINITY ? 0.f : exp_fast(l - mx) * inv_sum;
-  return sqrtf(log1pf(expf(-fabsf(l))) + fmaxf(l, 0.f));
+  // log(1 + e) = 2 atanh(z), z = e / (2 + e) <= 1/3; the terms left out are below 2e-8 of the sum
+  const float e = exp_fast(-fabsf(l)), z = e * rcp_fast(2.f + e), q = z * z;
+  float s = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+  s = fmaf(q, s, 1.f / 9.f);
+  s = fmaf(q, s, 1.f / 7.f);
+  s = fmaf(q, s, 1.f / 5.f);
+  s = fmaf(q, s, 1.f / 3.f);
+  s = fmaf(q * z, s, z);
+  return __fsqrt_rn(fmaf(2.f, s, fmaxf(l, 0.f)));
 }
 
 // Sorted in descending order (Batcher's odd-even merge sort, kN a power of two).
@@ -198,9 +208,10 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[kN]) {
           }
 }
 
-// The groups that stay, as a mask, in 64 bits; the layout of route_kernel.
+// The groups that stay, as a mask, in 64 bits; the layout of route_kernel.  `places`: those of this
+// lane's experts that may be among the two best of their group.
 template <typename T>
-__device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int log_lanes, double mx) {
+__device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int log_lanes, uint32_t places, double mx) {
   const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, per = a.E / a.n_group;
   const int g = lane >> log_lanes, i = lane & (lanes - 1);
   double sum = 1.0;
@@ -210,12 +221,14 @@ __device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int
     sum = warp_sum64(sum);
   }
   double b0 = -INFINITY, b1 = -INFINITY;
-  for (int j = i; g < a.n_group && j < per; j += lanes) {
-    double c = score64(a.score_fn, (double)to_f32<T>(row[g * per + j]), mx, sum) + (a.bias ? (double)a.bias[g * per + j] : 0.0);
+  for (; places; places &= places - 1) {
+    const int e = g * per + i + ((__ffs(places) - 1) << log_lanes);
+    double c = score64(a.score_fn, (double)to_f32<T>(row[e]), mx, sum) + (a.bias ? (double)a.bias[e] : 0.0);
     c = c == c ? c : -INFINITY;
     b1 = fmax(b1, fmin(b0, c));
     b0 = fmax(b0, c);
   }
+  __syncwarp();
   for (int o = 1; o < lanes; o <<= 1) {
     const double m0 = __shfl_xor_sync(kAll, b0, o), m1 = __shfl_xor_sync(kAll, b1, o);
     b1 = fmax(fmin(b0, m0), fmax(b1, m1));
@@ -236,15 +249,14 @@ __device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int
 // A token per warp at a time.  Group g has the kN * lanes slots of `lanes` = 32 / (n_group rounded
 // up to a power of two) neighbouring lanes, its expert j * lanes + i is lane i's j-th.
 // kFull: every lane has kN experts.
-template <typename T, int kN, bool kFull>
-__global__ void __launch_bounds__(kWarps * 32, kN <= 8 ? 4 : kN == 16 ? 2 : 1) route_kernel(RouteArgs a, int log_lanes, int index_bits) {
+template <typename T, int kN, bool kFull, int fn>
+__global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteArgs a, int log_lanes, int index_bits) {
   extern __shared__ double smem[];
   constexpr int kPlace = kN == 1 ? 0 : kN == 2 ? 1 : kN == 4 ? 2 : kN == 8 ? 3 : kN == 16 ? 4 : 5;
   constexpr float kU = 5.9604645e-8f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lanes = 1 << log_lanes, per = a.E / a.n_group, g = lane >> log_lanes, i = lane & (lanes - 1);
   const int e0 = g * per + i, count = g < a.n_group ? (per - i + lanes - 1) >> log_lanes : 0;  // this lane's experts
-  const int fn = a.score_fn;
   // 16-bit logits without a bias are whole in a key's upper half, and the expert's index in the
   // lower one puts equal ones in order; otherwise a key gives up the bits of the place in the lane.
   const bool whole = !a.bias && sizeof(T) == 2;
@@ -328,6 +340,7 @@ __global__ void __launch_bounds__(kWarps * 32, kN <= 8 ? 4 : kN == 16 ? 2 : 1) r
         k0 = max(k0, m0);
       }
       float v0 = value(k0), v1 = per > 1 ? value(k1) : 0.f;
+      const float second = per > 1 ? v1 : v0;
       float off = whole ? 0.f : (fabsf(v0) + fabsf(v1)) * cut;  // the bits that the keys left out
       if (!a.bias) {  // scores grow by less than the logit does, the softmax's in proportion to itself
         v0 = score32(fn, v0, mx, inv_sum);
@@ -348,8 +361,14 @@ __global__ void __launch_bounds__(kWarps * 32, kN <= 8 ? 4 : kN == 16 ? 2 : 1) r
       }
       const uint32_t next = __reduce_max_sync(kAll, gk);
       const float vl = value_of(last & ~31u), vn = value_of(next & ~31u);
-      if (!(vl - vn > 2.f * worst_off + 8e-6f * fabsf(vn)))  // 2^-17: the five bits of the group
-        kept = groups_of<T>(a, row, log_lanes, (double)mx);
+      if (!(vl - vn > 2.f * worst_off + 8e-6f * fabsf(vn))) {  // 2^-17: the five bits of the group
+        uint32_t places = 0;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (key[j] != 0u && !(value(key[j]) + fabsf(value(key[j])) * cut + 1e-37f < second - 2.f * blur))
+            places |= 1u << (whole ? ((int)(low - (key[j] & low)) - e0) >> log_lanes : (int)(key[j] & low));
+        kept = groups_of<T>(a, row, log_lanes, places, (double)mx);
+      }
       if (!((kept >> g) & 1u)) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) key[j] = 0u;
@@ -442,9 +461,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_wide_kernel(RouteArgs a) {
   }
 }
 
+using RouteKernel = void (*)(RouteArgs, int, int);
+template <typename T, int kN, bool kFull>
+RouteKernel pick_fn(int fn) {
+  return fn == DSV4_SCORE_SOFTMAX ? route_kernel<T, kN, kFull, DSV4_SCORE_SOFTMAX>
+         : fn == DSV4_SCORE_SIGMOID ? route_kernel<T, kN, kFull, DSV4_SCORE_SIGMOID>
+                                    : route_kernel<T, kN, kFull, DSV4_SCORE_SQRT_SOFTPLUS>;
+}
+// Full lanes are worth a kernel of their own (fewer tests) from 128 experts on.
 template <typename T, int kN>
-void (*pick(const RouteArgs& a))(RouteArgs, int, int) {
-  return a.E == 32 * kN && (a.n_group & (a.n_group - 1)) == 0 ? route_kernel<T, kN, true> : route_kernel<T, kN, false>;
+RouteKernel pick(const RouteArgs& a) {
+  constexpr bool kOwn = kN == 4 || kN == 8 || kN == 16;
+  return kOwn && a.E == 32 * kN && (a.n_group & (a.n_group - 1)) == 0 ? pick_fn<T, kN, kOwn>(a.score_fn) : pick_fn<T, kN, false>(a.score_fn);
 }
 
 template <typename T>
@@ -463,7 +491,8 @@ cudaError_t launch_type(const RouteArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (need > 32) return launch(route_wide_kernel<T>, blocks, kWarps * 32, smem, st, a);
-  return launch(fn, blocks < kBlocks ? blocks : kBlocks, kWarps * 32, smem, st, a, log_lanes, bits);
+  const int64_t held = (int64_t)sm_count() * ctas_of(need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : 32);
+  return launch(fn, blocks < held ? blocks : held, kWarps * 32, smem, st, a, log_lanes, bits);
 }
 
 }  // namespace
