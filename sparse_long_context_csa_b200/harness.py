@@ -11,7 +11,9 @@ A "step" is one pass of the hot path over one batch:
   output projection: dsv4_grouped_out_proj of the attention output (o_a_proj per head
                      group, then o_b_proj)
 PyTorch only allocates device memory and supplies the stream; every step of the
-method runs inside libdsv4.
+method runs inside libdsv4.  What follows the attention in a decoder layer is
+``moe_step``: the residual stream's norm, the routing and the experts' products in
+libdsv4, with the router's own product, a plain GEMM, from PyTorch between them.
 """
 from __future__ import annotations
 
@@ -245,3 +247,45 @@ def step_parts(w, params, x: dict, o: dict, stream=None, events=None) -> None:
         abi.dsv4_sparse_mqa_attn(params, x["q"], o["kv_rot"], o.get("pool"), o.get("idx"), x["sink"], x["pos"],
                                  None, o["out"], ws, stream=stream)
     mark("attention", 1)
+
+
+def moe_params(T, hidden, inter, E, topk, *, n_group=1, topk_group=1, score_fn=abi.SCORE_SQRT_SOFTPLUS, renorm=True,
+               routed_scale=1.0, swiglu_limit=0.0, eps=1e-6, eight_bit=False) -> abi.Dsv4MoeParams:
+    """dsv4_moe_params of a routed layer with bf16 activations and float32 router logits;
+    ``eight_bit``: the experts take the norm's e4m3 form (power-of-two scales)."""
+    p = abi.Dsv4MoeParams()
+    p.T, p.hidden, p.inter, p.E, p.topk = T, hidden, inter, E, topk
+    p.n_group, p.topk_group, p.score_fn, p.renorm = n_group, topk_group, score_fn, int(renorm)
+    p.scale_pow2 = int(eight_bit)
+    p.dtype, p.logits_dtype = abi.BF16, abi.F32
+    p.eps, p.routed_scale, p.swiglu_limit = eps, routed_scale, swiglu_limit
+    return p
+
+
+def moe_buffers(p: abi.Dsv4MoeParams, device="cuda") -> dict:
+    """Outputs and workspace of ``moe_step``."""
+    def new(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+    o = {"stream": new(p.T, p.hidden), "y": new(p.T, p.hidden), "out": new(p.T, p.hidden),
+         "logits": new(p.T, p.E, dtype=torch.float32), "ids": new(p.T, p.topk, dtype=torch.int32),
+         "weights": new(p.T, p.topk, dtype=torch.float32), "q": None, "q_scale": None,
+         "workspace": new(abi.dsv4_expert_mlp_workspace_bytes(p), dtype=torch.uint8)}
+    if p.scale_pow2:
+        o["q"] = new(p.T, p.hidden, dtype=torch.float8_e4m3fn)
+        o["q_scale"] = new(p.T, -(-p.hidden // 128), dtype=torch.float32)
+    return o
+
+
+def moe_step(p: abi.Dsv4MoeParams, x: dict, o: dict, stream=None) -> None:
+    """Enqueue what follows the attention's output projection in a routed layer:
+      stream = attn + residual stream, y = rms_norm(stream) * gamma  (with its e4m3 form)
+      logits = y router^T, ids and weights by score + bias, out = the experts' weighted products
+    x: attn, stream [T,hidden] bf16, gamma [hidden] bf16, router [E,hidden] float32, bias [E] float32
+    or None, w13 [E,2*inter,hidden], w2 [E,hidden,inter] bf16; o: ``moe_buffers``.  The router's
+    product runs on the current stream, which ``stream``, when given, has to be."""
+    abi.dsv4_add_rms_norm(p, x["attn"], x["stream"], x["gamma"], o["stream"], o["y"], o["q"], o["q_scale"], stream=stream)
+    torch.mm(o["y"].float(), x["router"].t(), out=o["logits"])
+    abi.dsv4_route_experts(p, o["logits"], x["bias"], o["ids"], o["weights"], stream=stream)
+    rows, scale = (o["y"], None) if o["q"] is None else (o["q"], o["q_scale"])
+    abi.dsv4_expert_mlp(p, rows, scale, o["ids"], o["weights"], x["w13"], x["w2"], o["out"], o["workspace"], stream=stream)

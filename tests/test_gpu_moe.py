@@ -407,73 +407,104 @@ def test_experts_are_the_same_bits_every_time(abi, T, E, topk):
 
 # ------------------------------------------------------------------ together
 
-def decoder_step(abi, s):
-    """norm -> router product -> routing -> experts, as a layer runs them after its attention."""
-    pn, pr, pe = s["p"]
-    abi.dsv4_add_rms_norm(pn, s["attn"], s["stream"], s["gamma"], s["stream_out"], s["y"], s["q"], s["scale"])
-    torch.matmul(s["y"].float(), s["router"], out=s["logits"])
-    abi.dsv4_route_experts(pr, s["logits"], s["bias"], s["ids"], s["w"])
-    abi.dsv4_expert_mlp(pe, s["q"], s["scale"], s["ids"], s["w"], s["w13"], s["w2"], s["out"], s["ws"])
+@pytest.fixture(scope="module")
+def harness(abi):
+    from sparse_long_context_csa_b200 import harness
+    return harness
 
 
-def decoder_state(abi, T, hidden=512, inter=256, E=16, topk=4, seed=0):
+def layer_inputs(p, seed):
     g = gen(seed)
     rnd = lambda *sh: torch.randn(sh, generator=g, device="cuda")  # noqa: E731
-    s = dict(attn=rnd(T, hidden).bfloat16(), stream=rnd(T, hidden).bfloat16(), gamma=(1 + 0.1 * rnd(hidden)).bfloat16(),
-             router=rnd(hidden, E) / hidden ** 0.5, bias=0.1 * rnd(E), w13=(rnd(E, 2 * inter, hidden) / hidden ** 0.5).bfloat16(),
-             w2=(rnd(E, hidden, inter) / inter ** 0.5).bfloat16())
-    s["stream_out"], s["y"], s["out"] = (torch.empty_like(s["attn"]) for _ in range(3))
-    s["q"] = torch.empty(T, hidden, dtype=torch.float8_e4m3fn, device="cuda")
-    s["scale"], s["logits"] = torch.empty(T, hidden // 128, device="cuda"), torch.empty(T, E, device="cuda")
-    s["ids"], s["w"] = torch.empty(T, topk, dtype=torch.int32, device="cuda"), torch.empty(T, topk, device="cuda")
-    pn = params(abi, T=T, hidden=hidden, scale_pow2=1)
-    pr = params(abi, T=T, E=E, topk=topk, n_group=4, topk_group=2, score_fn=abi.SCORE_SQRT_SOFTPLUS, renorm=1, routed_scale=1.5)
-    pe = params(abi, T=T, hidden=hidden, inter=inter, E=E, topk=topk, swiglu_limit=7.0)
-    s["p"] = (pn, pr, pe)
-    s["ws"] = torch.empty(abi.dsv4_expert_mlp_workspace_bytes(pe), dtype=torch.uint8, device="cuda")
-    return s
+    return dict(attn=rnd(p.T, p.hidden).bfloat16(), stream=rnd(p.T, p.hidden).bfloat16(), gamma=(1 + 0.1 * rnd(p.hidden)).bfloat16(),
+                router=rnd(p.E, p.hidden) / p.hidden ** 0.5, bias=0.1 * rnd(p.E),
+                w13=(rnd(p.E, 2 * p.inter, p.hidden) / p.hidden ** 0.5).bfloat16(),
+                w2=(rnd(p.E, p.hidden, p.inter) / p.inter ** 0.5).bfloat16())
 
 
-def check_decoder(s):
+def layer_params(harness, T, eight_bit):
+    return harness.moe_params(T, 512, 256, 16, 4, n_group=4, topk_group=2, routed_scale=1.5, swiglu_limit=7.0, eight_bit=eight_bit)
+
+
+def check_layer(p, x, o):
     """Each operator against the formula on the inputs that it was given."""
-    check_norm(s["attn"], s["stream"], s["gamma"], 1e-6, s["stream_out"], s["y"], s["q"], s["scale"], 1)
-    ids, w = O.route(f64(s["logits"]), f64(s["bias"]), fn="sqrt_softplus", topk=s["ids"].shape[1], n_group=4, topk_group=2,
-                     renorm=True, routed_scale=1.5)
-    np.testing.assert_array_equal(s["ids"].cpu().numpy(), ids)
-    assert np.allclose(f64(s["w"]), w, rtol=1e-5)
-    ref, tol = experts_reference(s["q"], s["scale"], s["ids"], s["w"], s["w13"], s["w2"], 7.0, False)
-    assert bool(((s["out"].double() - ref).abs() <= tol).all())
+    check_norm(x["attn"], x["stream"], x["gamma"], 1e-6, o["stream"], o["y"], o["q"], o["q_scale"], p.scale_pow2)
+    ids, w = O.route(f64(o["logits"]), f64(x["bias"]), fn="sqrt_softplus", topk=p.topk, n_group=4, topk_group=2, renorm=True,
+                     routed_scale=1.5)
+    np.testing.assert_array_equal(o["ids"].cpu().numpy(), ids)
+    assert np.allclose(f64(o["weights"]), w, rtol=1e-5)
+    rows, scale = (o["y"], None) if o["q"] is None else (o["q"], o["q_scale"])
+    ref, tol = experts_reference(rows, scale, o["ids"], o["weights"], x["w13"], x["w2"], 7.0, False)
+    assert bool(((o["out"].double() - ref).abs() <= tol).all())
 
 
-@pytest.mark.parametrize("T", [1, 7, 64, 513])
-def test_the_operators_together(abi, T):
-    s = decoder_state(abi, T, seed=T)
-    decoder_step(abi, s)
-    check_decoder(s)
+@pytest.mark.parametrize("eight_bit", [False, True])
+@pytest.mark.parametrize("T", [1, 7, 64, 513, 1100])
+def test_the_operators_together(abi, harness, T, eight_bit):
+    p = layer_params(harness, T, eight_bit)
+    x, o = layer_inputs(p, T), harness.moe_buffers(p)
+    harness.moe_step(p, x, o)
+    check_layer(p, x, o)
+    abi.dsv4_device_check()
 
 
 @pytest.mark.parametrize("T", [1, 5, 130])
-def test_captured_and_replayed_on_another_stream(abi, T):
-    s = decoder_state(abi, T, seed=T)
+def test_captured_and_replayed_on_another_stream(abi, harness, T):
+    p = layer_params(harness, T, True)
+    x, o = layer_inputs(p, T), harness.moe_buffers(p)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        decoder_step(abi, s)                       # warm-up outside the capture
+        harness.moe_step(p, x, o)                  # warm-up outside the capture
         side.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            decoder_step(abi, s)
+            harness.moe_step(p, x, o)
     for seed in (1, 2):
-        fresh = decoder_state(abi, T, seed=100 + seed)
-        s["attn"].copy_(fresh["attn"])
-        s["stream"].copy_(fresh["stream"])
-        s["bias"].copy_(fresh["bias"])
+        fresh = layer_inputs(p, 100 + seed)
+        for n in ("attn", "stream", "bias"):
+            x[n].copy_(fresh[n])
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
             graph.replay()
             graph.replay()                         # two in a row share the workspace
         torch.cuda.synchronize()
-        check_decoder(s)
+        check_layer(p, x, o)
+
+
+def test_two_graphs_share_a_workspace(abi):
+    """Calls of other sizes captured into two graphs, replayed in turn over one workspace."""
+    ins = [experts_inputs(T, 256, 128, 8, k, T) for T, k in ((90, 2), (2, 4), (2100, 2))]
+    want = [run_experts(abi, i).clone() for i in ins]
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    outs = [torch.full_like(w, 5.0) for w in want]
+    graphs = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for i, o in zip(ins, outs):
+            run_experts(abi, i, out=o, ws=ws)
+            side.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                run_experts(abi, i, out=o, ws=ws)
+            graphs.append(graph)
+        for o in outs:
+            o.fill_(5.0)
+        for _ in range(3):
+            for k in (0, 1, 2, 1, 0):
+                graphs[k].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_experts_saturated_gates(abi, T):
+    """Gates far below zero (silu underflows) and far above, with and without the clamp."""
+    x, _, ids, w, w13, w2 = experts_inputs(T, 128, 64, 4, 2, 3)
+    ins = (x, None, ids, w, (60 * w13.float()).bfloat16(), w2)
+    check_experts(abi, ins)
+    check_experts(abi, ins, limit=10.0)
 
 
 def test_two_calls_at_once_with_a_workspace_each(abi):
