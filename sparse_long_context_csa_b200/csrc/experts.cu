@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "moe.h"
@@ -495,9 +497,13 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(ExpertArgs a, 
 // some 550 clocks, so that stages of 4, 8, 16 and 32 KB stream 2.1, 4.1, 6.9 and 7.0 TB/s (805 MB,
 // nothing else done).  96 KB of ring let the CTAs of both products fit an SM, so that the second
 // one fills its ring while the first one ends.  The eight consumer warps divide a row's channels:
-// each keeps its part of the tokens' rows in registers and reads nothing but weights.  A warp's
-// part of a dot goes to shared memory; every 32 items the warps meet and the parts are summed,
-// always in the same order (meeting at every stage held the stream to 3.6 TB/s).
+// each keeps its part of the tokens' rows in registers and reads nothing but weights, two channels
+// a multiply-add.  A warp's part of a dot goes to shared memory; every 32 items the warps meet and
+// the parts are summed, always in the same order.  What bounds it is the consumers' latency: one
+// token of six experts (4096 x 2048, 302 MB) takes 58 us, 5.2 TB/s (65 us with single multiply-adds,
+// 85 us with a meeting at every stage).
+// More tokens than three go through the tensor cores: four of six experts take 181 us there and
+// 278 us here, where the rows of more than kFewRows pairs of an expert are streamed again.
 constexpr int kFewPairs = 32, kFewTokens = 3, kFewWarps = 8, kFewRows = 2, kFlush = 32;
 constexpr int kFewThreads = (kFewWarps + 1) * 32;
 constexpr uint32_t kFewRing = 96 * 1024;
@@ -539,14 +545,25 @@ struct FewShape {
   }
 };
 
-__device__ __forceinline__ void unpack(const uint4& v, float* f) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Two fp32 values in a register pair, and two fused multiply-adds at once.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum_of(uint64_t p) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+  return lo + hi;
+}
+// Two bf16 values of a word.
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) { return pair_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    tc::smem_u32(dst)),
@@ -612,9 +629,12 @@ __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& 
   // the items between two meetings: whole stages, or one stage where it has more
   const int flush = max(kFlush / step, 1) * step;
   const int value = lane / kPer;  // this lane's of the kV dots: [turn][gate, up][pair]
+  const int value_item = value / (kNR * kR) * fs.side + g, value_dot = value % (kNR * kR);
+  const uint32_t hop = fs.side * fs.row_bytes;
+  const bool whole_part = (kw + 1) * 32 * kP <= K8;  // no lane of the warp is behind the row's end
   for (int first = 0; first < rows; first += kR) {
     // this lane's part of the pairs' rows
-    float x[kR][kP][8];
+    uint64_t x[kR][kP][4];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       const int slot = max(nth_bit(mine, first + r), 0);
@@ -634,7 +654,9 @@ __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& 
               v = static_cast<const uint4*>(a.x)[t * K8 + i];
           }
         }
-        unpack(v, x[r][q]);
+        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[r][q][j] = pair_of(words[j]);
       }
     }
     for (int i0 = 0; i0 < count; i0 += flush) {
@@ -642,32 +664,42 @@ __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& 
       float (*part)[2 * kFewRows][kFewWarps] = sh->part[at.part];
       bool ok = true;
       for (int i = 0; i < n && ok; i += step) {
-        float acc[kV];
+        uint64_t acc[kV];
 #pragma unroll
-        for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+        for (int v = 0; v < kV; ++v) acc[v] = 0;
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sh->full[at.stage], at.phase, kWaitLimit));
-        const uint8_t* stage = smem + at.stage * fs.stage_bytes;
+        // Rows that a last stage lacks are whatever the ring holds: their dots are not looked at.
+        const uint8_t* w0 = smem + at.stage * fs.stage_bytes + g * fs.row_bytes + piece * 16;
+        auto dots = [&](auto whole) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-          for (int nr = 0; nr < kNR; ++nr) {
-            const uint4* w = reinterpret_cast<const uint4*>(stage + (uint32_t)((nr * kBatch + b) * fs.side + g) * fs.row_bytes);
+          for (int item = 0; item < kNR * kBatch; ++item) {
+            const int v = (item % kBatch * kNR + item / kBatch) * kR;  // rows lie by (gate, up), turn
 #pragma unroll
             for (int q = 0; q < kP; ++q) {
-              if (piece + 32 * q >= K8 || i + b * fs.side + g >= n) continue;
-              float f[8];
-              unpack(w[piece + 32 * q], f);
+              if (!whole.value && piece + 32 * q >= K8) continue;
+              const uint4 w = *reinterpret_cast<const uint4*>(w0 + item * hop + q * 512);
+              const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-              for (int r = 0; r < kR; ++r)
+              for (int j = 0; j < 4; ++j) {
+                const uint64_t two = pair_of(words[j]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[(b * kNR + nr) * kR + r] = fmaf(f[j], x[r][q][j], acc[(b * kNR + nr) * kR + r]);
+                for (int r = 0; r < kR; ++r) acc[v + r] = fma2(two, x[r][q][j], acc[v + r]);
+              }
             }
           }
+        };
+        if (whole_part)
+          dots(std::true_type{});
+        else
+          dots(std::false_type{});
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh->empty[at.stage]);
         at.next(fs.stages);
-        const float dot = sum_transposed<kV>(acc);
-        if (lane % kPer == 0) part[i + value / (kNR * kR) * fs.side + g][value % (kNR * kR)][kw] = dot;
+        float sums[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) sums[v] = sum_of(acc[v]);
+        const float dot = sum_transposed<kV>(sums);
+        if (lane % kPer == 0) part[i + value_item][value_dot][kw] = dot;
       }
       at.part ^= 1;
       if (!tc::named_bar_and(1, workers, ok)) return false;
