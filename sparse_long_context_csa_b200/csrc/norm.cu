@@ -29,8 +29,18 @@ __device__ __forceinline__ float group_scale(float amax, int pow2) {
   return s;
 }
 
-// y / s; the reciprocal of a very small scale would leave fp32's range.
-__device__ __forceinline__ float scaled(float y, float s, float inv) { return s >= 0x1p-100f ? y * inv : y / s; }
+// v / s, by the reciprocal but where that leaves fp32's normal range.
+template <int kN>
+__device__ __forceinline__ void divide(float (&v)[kN], float s) {
+  if (s >= 0x1p-100f) {
+    const float inv = __frcp_rn(s);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] *= inv;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] /= s;
+  }
+}
 
 template <typename T>
 struct Piece;  // 16 bytes of a row
@@ -132,14 +142,15 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormArgs a, int per) {
     for (int j = 0; j < kN; ++j) most = max(most, __float_as_uint(r[v][j]) & 0x7fffffffu);
 #pragma unroll
     for (int o = kScaleGroup / kN / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const float s = group_scale(__uint_as_float(i < n ? most : 0u), a.scale_pow2), inv = 1.f / s;
+    const float s = group_scale(__uint_as_float(i < n ? most : 0u), a.scale_pow2);
     if (i >= n) continue;
+    divide(r[v], s);
     if (i % (kScaleGroup / kN) == 0) a.yscale[row * groups + i / (kScaleGroup / kN)] = s;
     uint32_t q[kN / 4];
 #pragma unroll
     for (int j = 0; j < kN; j += 4) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(scaled(r[v][j], s, inv), scaled(r[v][j + 1], s, inv)), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(scaled(r[v][j + 2], s, inv), scaled(r[v][j + 3], s, inv)), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(r[v][j], r[v][j + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(r[v][j + 2], r[v][j + 3]), __NV_SATFINITE, __NV_E4M3);
       q[j / 4] = lo | (hi << 16);
     }
     uint8_t* out = a.yq + (row * n + i) * kN;
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   }
   if (!live) return;
   const float inv_rms = rsqrtf(sq / (float)a.hidden + a.eps);
-  auto finish = [&](int g, float* v) {
+  auto finish = [&](int g, float (&v)[4]) {
     uint32_t most = 0;  // of the magnitudes' bits: a NaN is above infinity
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -212,12 +223,13 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
       most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
     }
     if (!a.yq) return;
-    const float s = group_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, most)), a.scale_pow2), inv = 1.f / s;
+    const float s = group_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, most)), a.scale_pow2);
     if (lane == 0) a.yscale[row * groups + g] = s;
+    divide(v, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = g * kScaleGroup + i * 32 + lane;
-      if (c < a.hidden) a.yq[base + c] = __nv_cvt_float_to_fp8(scaled(v[i], s, inv), __NV_SATFINITE, __NV_E4M3);
+      if (c < a.hidden) a.yq[base + c] = __nv_cvt_float_to_fp8(v[i], __NV_SATFINITE, __NV_E4M3);
     }
   };
   if (kG > 0) {
