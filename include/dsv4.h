@@ -347,14 +347,14 @@ typedef enum { DSV4_SCORE_SOFTMAX = 0, DSV4_SCORE_SIGMOID = 1, DSV4_SCORE_SQRT_S
  * r, its sum of squares and y are formed in 32 bits; r, y and q are each rounded once, from
  * those.  The last group may be shorter than 128.  The scale of an all-zero group is 1; with
  * scale_pow2 the scales are rounded up to a power of two (q * s is then exact in bf16).
- * A NaN in a row makes the row NaN.
+ * A NaN in a row makes the row NaN; so do infinities, and zeros with eps 0, as the formula says.
  *
  *   x         [T,hidden] T
  *   residual  [T,hidden] T or NULL (r = x)
  *   weight    [hidden] T
  *   res_out   [T,hidden] T or NULL   out: r (may be x or residual itself)
  *   y         [T,hidden] T or NULL   out (may be x or residual itself, not res_out)
- *   yq        [T,hidden] e4m3 or NULL                out: q
+ *   yq        [T,hidden] e4m3 or NULL                out: q (memory of its own)
  *   yscale    [T,ceil(hidden/128)] f32, NULL without yq   out: s
  * At least one of y and yq.  Uses T, hidden, eps, scale_pow2 and dtype.  Any hidden >= 1;
  * rows of whole 16-byte pieces are read fastest.  Validates on the host (DSV4_ERR_ARG /

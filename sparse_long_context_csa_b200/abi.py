@@ -161,6 +161,12 @@ def _dense(fn: str, stream, *tensors) -> list:
     return out
 
 
+def _four_bytes(fn: str, what: str, t) -> None:
+    """ids and weights as torch.topk returns them (int64, the logits' type) are not what the kernels read."""
+    if t is not None and type(t) is not int and t.element_size() != 4:
+        raise Dsv4Error(fn, 1, f"{what} of type {t.dtype} instead of 32 bits")
+
+
 def _check(fn: str, st: int) -> None:
     if st != 0:
         raise Dsv4Error(fn, st, load().dsv4_status_string(st).decode())
@@ -269,8 +275,10 @@ def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=N
 
 def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
     """The topk experts of each token (ids, in descending order of score + bias) and their weights."""
-    _check("dsv4_route_experts", load().dsv4_route_experts(
-        ctypes.byref(params), *_dense("dsv4_route_experts", stream, logits, bias, ids, weights)))
+    args = _dense("dsv4_route_experts", stream, logits, bias, ids, weights)
+    _four_bytes("dsv4_route_experts", "ids", ids)
+    _four_bytes("dsv4_route_experts", "weights", weights)
+    _check("dsv4_route_experts", load().dsv4_route_experts(ctypes.byref(params), *args))
 
 
 def dsv4_expert_mlp_workspace_bytes(params: Dsv4MoeParams) -> int:
@@ -282,6 +290,8 @@ def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, w
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \
         else (ws_bytes or 0)
     *ptrs, stream = _dense("dsv4_expert_mlp", stream, x, x_scale, ids, weights, w13, w2, out, workspace)
+    _four_bytes("dsv4_expert_mlp", "ids", ids)
+    _four_bytes("dsv4_expert_mlp", "weights", weights)
     _check("dsv4_expert_mlp", load().dsv4_expert_mlp(ctypes.byref(params), *ptrs, ws_bytes, stream))
 
 

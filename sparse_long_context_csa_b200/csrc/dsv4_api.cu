@@ -212,7 +212,7 @@ const char* dsv4_status_string(dsv4_status s) {
   return "unknown status";
 }
 
-int32_t dsv4_version(void) { return 100; }
+int32_t dsv4_version(void) { return 101; }
 
 uint64_t dsv4_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
@@ -485,6 +485,7 @@ dsv4_status dsv4_add_rms_norm(const dsv4_moe_params* p, const void* x, const voi
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return DSV4_ERR_ALIGN;
   if (res_out && res_out == y) return DSV4_ERR_ARG;
+  if (yq && (yq == x || yq == residual || yq == res_out || yq == y || yq == yscale)) return DSV4_ERR_ARG;
   NormArgs a{};
   a.T = p->T; a.hidden = p->hidden; a.scale_pow2 = p->scale_pow2; a.eps = p->eps;
   a.x = x; a.residual = residual; a.weight = weight; a.res_out = res_out; a.y = y;

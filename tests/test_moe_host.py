@@ -49,6 +49,8 @@ def test_norm_refusals(abi):
     assert _norm(abi, p, y=None, yq=None, yscale=None) == ARG      # no output
     assert _norm(abi, p, yq=None) == ARG                           # scales without the 8-bit form
     assert _norm(abi, p, res_out=FAKE, y=FAKE) == ARG              # two outputs in one place
+    for n in ("x", "residual", "res_out", "y", "yscale"):           # rows of half the bytes over another's
+        assert _norm(abi, p, **{n: FAKE, "yq": FAKE}) == ARG, n
     for n in ("x", "residual", "weight", "res_out", "y", "yq", "yscale"):
         assert _norm(abi, p, **{n: FAKE + 8}) == ALIGN
 
@@ -147,3 +149,31 @@ def test_binding_refuses_tensors_that_the_kernels_cannot_read(abi, monkeypatch):
     with pytest.raises(abi.Dsv4Error) as e:                       # on cuda:0 while cuda:1 is current
         abi.dsv4_route_experts(_params(abi), Strided(), None, FAKE, FAKE, stream=0)
     assert e.value.status == ARG and "current" in str(e.value)
+
+
+@pytest.mark.parametrize("size", [2, 8])
+def test_binding_refuses_ids_and_weights_that_are_not_of_32_bits(abi, monkeypatch, size):
+    """What torch.topk returns: of int64 ids, read as 32 bits, every other one would be 0."""
+    class Choice:
+        device, dtype = "cuda:0", f"{8 * size} bits"
+
+        def get_device(self):
+            return 0
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return FAKE
+
+        def element_size(self):
+            return size
+
+    monkeypatch.setattr(abi, "_now", lambda: (0, 0))
+    for ids, weights in ((Choice(), FAKE), (FAKE, Choice())):
+        for call in (lambda: abi.dsv4_route_experts(_params(abi), FAKE, None, ids, weights, stream=0),
+                     lambda: abi.dsv4_expert_mlp(_params(abi), FAKE, None, ids, weights, FAKE, FAKE, FAKE, FAKE, ws_bytes=1,
+                                                 stream=0)):
+            with pytest.raises(abi.Dsv4Error) as e:
+                call()
+            assert e.value.status == ARG and f"{8 * size} bits" in str(e.value)
