@@ -321,13 +321,17 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
     const int64_t now = t;
     if (t + (int64_t)gridDim.x * kWarps < a.T) load(t + (int64_t)gridDim.x * kWarps);  // the next token's
     sort_down<kN>(key);
-    // fp32's rounding: a score is within 12 u (u = 2^-24) of the largest score + |bias|, its sum with
-    // the bias within one more; the softmax's sum over up to 32 values a lane and 5 steps brings
-    // 50 u.  Without a bias the logits themselves are compared.
+    // fp32's rounding, in u = 2^-24, with m the largest score + |bias|: a score s has |ln s| u of itself
+    // from exp's argument (the softmax's twice that), which for m above e^-7 stays below 8 m u, and 7 u
+    // of itself from exp, the sum and the reciprocal; its sum with the bias is within one more.  The
+    // softmax's sum over up to 32 values a lane and 5 steps, of such terms, brings 60 u.  Where all
+    // scores are small, |ln s| goes up to 88 before s ends.  Without a bias the logits themselves are
+    // compared.
     float blur = 0.f;
     if (a.bias) {
       const float top = value(__reduce_max_sync(kAll, key[0]));
-      blur = (fn == DSV4_SCORE_SOFTMAX ? 64.f : 16.f) * kU * (fabsf(top) + 2.f * most_bias);
+      const float m = fabsf(top) + 2.f * most_bias;
+      blur = (fn == DSV4_SCORE_SOFTMAX ? (m > 1e-3f ? 96.f : 256.f) : m > 1e-3f ? 16.f : 128.f) * kU * m;
     }
     const T* row = static_cast<const T*>(a.logits) + now * a.E;
 
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
         v1 = per > 1 ? score32(fn, v1, mx, inv_sum) : 0.f;
         if (fn == DSV4_SCORE_SOFTMAX) off *= v0 + v1;
       }
-      off += 2.f * blur + 64.f * kU * (fabsf(v0) + fabsf(v1));
+      off += 2.f * blur + 256.f * kU * (fabsf(v0) + fabsf(v1));
       float best = v0 + v1;
       if (!(best == best)) best = -INFINITY;
       const float worst_off = warp_max(off < INFINITY ? off : 0.f);
@@ -361,7 +365,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
       }
       const uint32_t next = __reduce_max_sync(kAll, gk);
       const float vl = value_of(last & ~31u), vn = value_of(next & ~31u);
-      if (!(vl - vn > 2.f * worst_off + 8e-6f * fabsf(vn))) {  // 2^-17: the five bits of the group
+      // 2^-17: the five bits of the group; an infinite score or bias says nothing about the others
+      if (!(vl - vn > 2.f * worst_off + 8e-6f * fabsf(vn) + 1e-37f) || !(blur < INFINITY)) {
         uint32_t places = 0;
 #pragma unroll
         for (int j = 0; j < kN; ++j)

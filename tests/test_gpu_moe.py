@@ -113,7 +113,9 @@ def test_norm(abi, T, hidden, dtype):
         check_norm(x, residual, weight, 1e-5, *cut, pow2)
 
 
-@pytest.mark.parametrize("T,hidden,dtype", [(5, 4096, torch.bfloat16), (6, 129, torch.float32), (3, 8200, torch.bfloat16)])
+@pytest.mark.parametrize("T,hidden,dtype", [(5, 4096, torch.bfloat16), (6, 129, torch.float32), (3, 8200, torch.bfloat16),
+                                            (9, 333, torch.bfloat16), (3, 5001, torch.bfloat16), (2, 40000, torch.bfloat16),
+                                            (3, 1999, torch.float32)])
 def test_norm_in_place(abi, T, hidden, dtype):
     """The residual stream updated where it lies, and y written over x."""
     g = gen(9)
@@ -237,10 +239,34 @@ def test_route_masked_and_non_finite(abi):
     for fn in ("sigmoid", "sqrt_softplus"):
         check_route(abi, nan, None, fn, 5, renorm=0)
         check_route(abi, nan, 0.1 * torch.randn(E, generator=gen(9), device="cuda"), fn, 5, 4, 2, 0)
+    # an expert that everyone has to take does not blur the choice among the others: two experts of
+    # equal biases and neighbouring logits in groups of their own
+    must = torch.zeros(E, device="cuda")
+    must[0] = inf
+    close = logits[6:7].repeat(64, 1)
+    close[:, 10:] *= 0.01
+    close[:, 10], close[:, 11], close[:, 20], close[:, 21] = 3.0, 2.0, 3.0, 2.0
+    close[:, 20] += 2.0 ** -21 * (torch.arange(64, device="cuda") % 5 - 2)
+    check_route(abi, close, must, "sigmoid", 3, 4, 2, 0)
     # a bias of -inf takes an expert out
     bias = torch.zeros(E, device="cuda")
     bias[:35] = -inf
     check_route(abi, logits, bias, "sigmoid", 5)
+
+
+@pytest.mark.parametrize("fn", ["softmax", "sigmoid", "sqrt_softplus"])
+@pytest.mark.parametrize("groups,kept", [(1, 1), (8, 3)])
+def test_route_neighbours_of_small_scores(abi, fn, groups, kept):
+    """Scores of about e^-30, where exp's argument rounds away as much as neighbouring logits differ."""
+    T, E = 64, 128
+    g = gen(21)
+    steps = torch.stack([torch.randperm(E, generator=g, device="cuda") for _ in range(T)])
+    logits = -30.0 - 2.0 ** -19 * steps                         # neighbours in fp32
+    bias = torch.zeros(E, device="cuda")
+    if fn == "softmax":
+        logits[:, 5], bias[5] = 0.0, -float("inf")             # nearly all of the sum, not to be chosen
+    check_route(abi, logits, bias, fn, 6, groups, kept, 0)
+    check_route(abi, logits, None, fn, 6, groups, kept, 0)
 
 
 # ------------------------------------------------------------------ experts
@@ -326,7 +352,8 @@ EXPERTS = [  # T, hidden, inter, E, topk
     (1000, 528, 304, 8, 4), (2049, 512, 512, 16, 2),
     (2, 4112, 4112, 3, 2), (3, 8192, 272, 4, 3), (1, 8208, 64, 3, 2), (2, 64, 8208, 3, 2),  # widths at the few-token path's ends
     (3, 512, 256, 2, 2), (4, 512, 256, 2, 2), (3, 16, 16, 2, 11), (1, 48, 16, 40, 33),      # tokens and pairs at its ends
-    (272, 256, 128, 1, 1), (511, 128, 64, 1, 1), (600, 192, 80, 511, 7), (600, 192, 80, 512, 7), (1025, 128, 32, 1, 4)]
+    (272, 256, 128, 1, 1), (511, 128, 64, 1, 1), (600, 192, 80, 511, 7), (600, 192, 80, 512, 7), (1025, 128, 32, 1, 4),
+    (1030, 2064, 32, 4, 3), (2050, 2064, 16, 3, 2), (4100, 4112, 16, 2, 2)]                 # rows wider than a CTA, and than L2 keeps
 
 
 @pytest.mark.parametrize("T,hidden,inter,E,topk", EXPERTS)
