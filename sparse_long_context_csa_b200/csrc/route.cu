@@ -15,13 +15,22 @@
 namespace dsv4 {
 namespace {
 
-constexpr int kWarps = 8;
+// Small CTAs, of which an SM holds as many as the registers allow: for 8 experts a lane 20 warps of
+// 96 registers (16384 tokens, 256 experts in 8 groups: 17.6 us; CTAs of 8 warps, 24 warps of 80
+// registers, some spilled: 18.9 us; 16 warps: 18.9 us).
+constexpr int kWarps = 2;
 // CTAs of a kernel with kN experts a lane that an SM holds at once (its registers).
-constexpr int ctas_of(int kN) { return kN <= 4 ? 4 : kN == 8 ? 3 : kN == 16 ? 2 : 1; }
+constexpr int ctas_of(int kN) { return kN <= 4 ? 12 : kN == 8 ? 10 : kN == 16 ? 8 : 4; }
 constexpr unsigned kAll = 0xffffffffu;
 
 // Doubles of shared memory per warp: a value per expert, or 32 integers.
 __host__ __device__ constexpr int scratch_of(int E) { return E < 16 ? 16 : E; }
+// Words of shared memory per warp for the lanes' sorted lists, without their first two values and
+// with three zeros behind the last.  A list that loses its first value then moves one word instead
+// of all (16384 tokens, 256 experts in 8 groups: 17.1 us, 17.6 in registers; 512: 36.4 and 42.9; of
+// four values a lane no faster).
+constexpr int kListed = 8;  // from this many values on
+__host__ __device__ constexpr int list_of(int kN) { return kN < kListed ? 0 : 32 * (kN + 1); }
 
 // ---------------------------------------------------------------- 64 bits
 
@@ -209,11 +218,11 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[kN]) {
 }
 
 // The groups that stay, as a mask, in 64 bits; the layout of route_kernel.  `places`: those of this
-// lane's experts that may be among the two best of their group.
+// lane's experts e0 + (place << shift) that may be among the two best of their group.
 template <typename T>
-__device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int log_lanes, uint32_t places, double mx) {
-  const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, per = a.E / a.n_group;
-  const int g = lane >> log_lanes, i = lane & (lanes - 1);
+__device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int log_lanes, int e0, int shift, uint32_t places,
+                                           double mx) {
+  const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, per = a.E / a.n_group, g = lane >> log_lanes;
   double sum = 1.0;
   if (a.score_fn == DSV4_SCORE_SOFTMAX) {
     sum = 0.0;
@@ -222,7 +231,7 @@ __device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int
   }
   double b0 = -INFINITY, b1 = -INFINITY;
   for (; places; places &= places - 1) {
-    const int e = g * per + i + ((__ffs(places) - 1) << log_lanes);
+    const int e = e0 + ((__ffs(places) - 1) << shift);
     double c = score64(a.score_fn, (double)to_f32<T>(row[e]), mx, sum) + (a.bias ? (double)a.bias[e] : 0.0);
     c = c == c ? c : -INFINITY;
     b1 = fmax(b1, fmin(b0, c));
@@ -246,9 +255,24 @@ __device__ __noinline__ unsigned groups_of(const RouteArgs& a, const T* row, int
   return kept;
 }
 
+// The kN logits from p on, in pieces of up to 16 bytes.
+template <typename T, int kN>
+__device__ __forceinline__ void load_row(const T* p, float (&l)[kN]) {
+  constexpr int kBytes = kN * sizeof(T) < 16 ? kN * sizeof(T) : 16, kPer = kBytes / sizeof(T);
+  struct alignas(kBytes) Pack {
+    T v[kPer];
+  };
+#pragma unroll
+  for (int j = 0; j < kN; j += kPer) {
+    const Pack v = *reinterpret_cast<const Pack*>(p + j);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) l[j + i] = to_f32<T>(v.v[i]);
+  }
+}
+
 // A token per warp at a time.  Group g has the kN * lanes slots of `lanes` = 32 / (n_group rounded
 // up to a power of two) neighbouring lanes, its expert j * lanes + i is lane i's j-th.
-// kFull: every lane has kN experts.
+// kFull: every lane has kN experts, which then are neighbours.
 template <typename T, int kN, bool kFull, int fn>
 __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteArgs a, int log_lanes, int index_bits) {
   extern __shared__ double smem[];
@@ -256,7 +280,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
   constexpr float kU = 5.9604645e-8f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lanes = 1 << log_lanes, per = a.E / a.n_group, g = lane >> log_lanes, i = lane & (lanes - 1);
-  const int e0 = g * per + i, count = g < a.n_group ? (per - i + lanes - 1) >> log_lanes : 0;  // this lane's experts
+  const int count = g < a.n_group ? (per - i + lanes - 1) >> log_lanes : 0;  // this lane's experts: e0 + (j << shift)
+  const int e0 = kFull ? lane * kN : g * per + i, shift = kFull ? 0 : log_lanes;
   // 16-bit logits without a bias are whole in a key's upper half, and the expert's index in the
   // lower one puts equal ones in order; otherwise a key gives up the bits of the place in the lane.
   const bool whole = !a.bias && sizeof(T) == 2;
@@ -265,21 +290,31 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
   auto value = [&](uint32_t k) { return (k & ~low) == lowest ? -INFINITY : value_of(k & ~low); };
   const float cut = __int_as_float((127 + bits - 23) << 23);  // what a key leaves out, of the value
 
+  const uint32_t self = 1u << lane, upto = self | (self - 1);
   double* scratch = smem + (size_t)warp * scratch_of(a.E);
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + (size_t)kWarps * scratch_of(a.E)) + warp * list_of(kN) + lane;
+  if constexpr (kN >= kListed) {
+#pragma unroll
+    for (int j = kN - 2; j < kN + 1; ++j) list[32 * j] = 0u;
+  }
   wait_for_previous();
   int64_t t = (int64_t)blockIdx.x * kWarps + warp;
   float bias[kN], most_bias = 0.f;
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
-    bias[j] = a.bias && j < count ? a.bias[e0 + j * lanes] : 0.f;
+    bias[j] = a.bias && (kFull || j < count) ? a.bias[e0 + (j << shift)] : 0.f;
     if (fabsf(bias[j]) < INFINITY) most_bias = fmaxf(most_bias, fabsf(bias[j]));
   }
   if (a.bias) most_bias = warp_max(most_bias);
   float l[kN];
   auto load = [&](int64_t token) {
     const T* p = static_cast<const T*>(a.logits) + token * a.E + e0;
+    if constexpr (kFull) {
+      load_row<T, kN>(p, l);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kN; ++j, p += lanes) l[j] = kFull || j < count ? to_f32<T>(*p) : -INFINITY;
+      for (int j = 0; j < kN; ++j, p += lanes) l[j] = j < count ? to_f32<T>(*p) : -INFINITY;
+    }
   };
   if (t < a.T) load(t);
   for (; t < a.T; t += (int64_t)gridDim.x * kWarps) {
@@ -304,7 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
     } else {
       const float floor_l = fn == DSV4_SCORE_SOFTMAX ? mx - 745.f : -745.f;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) l[j] = l[j] < floor_l ? -INFINITY : l[j];
+      for (int j = 0; j < kN; ++j) l[j] = l[j] < floor_l ? -INFINITY : l[j] + 0.f;  // -0 is 0
     }
     if (lost) {
 #pragma unroll
@@ -313,9 +348,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
     uint32_t key[kN];
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      const uint32_t place = whole ? low - (uint32_t)(e0 + j * lanes) : (uint32_t)j;
-      // fmaxf: a NaN is -inf; + 0: -0 is 0
-      key[j] = (order_of(fmaxf(l[j], -INFINITY) + 0.f) & ~low) | place;
+      const uint32_t place = whole ? low - (uint32_t)(e0 + (j << shift)) : (uint32_t)j;
+      key[j] = (order_of(fmaxf(l[j], -INFINITY)) & ~low) | place;  // a NaN is -inf
       if (!kFull && j >= count) key[j] = 0u;
     }
     const int64_t now = t;
@@ -330,7 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
     float blur = 0.f;
     if (a.bias) {
       const float top = value(__reduce_max_sync(kAll, key[0]));
-      const float m = fabsf(top) + 2.f * most_bias;
+      const float m = fabsf(top) + most_bias;
       blur = (fn == DSV4_SCORE_SOFTMAX ? (m > 1e-3f ? 96.f : 256.f) : m > 1e-3f ? 16.f : 128.f) * kU * m;
     }
     const T* row = static_cast<const T*>(a.logits) + now * a.E;
@@ -346,33 +380,37 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
       float v0 = value(k0), v1 = per > 1 ? value(k1) : 0.f;
       const float second = per > 1 ? v1 : v0;
       float off = whole ? 0.f : (fabsf(v0) + fabsf(v1)) * cut;  // the bits that the keys left out
-      if (!a.bias) {  // scores grow by less than the logit does, the softmax's in proportion to itself
+      if (a.bias) {
+        off += 2.f * blur + 2.f * kU * (fabsf(v0) + fabsf(v1));
+      } else {  // scores grow by less than the logit does, the softmax's in proportion to itself
+        const float x = fminf(fabsf((fn == DSV4_SCORE_SOFTMAX ? mx : 0.f) - (per > 1 ? v1 : v0)), 90.f);
         v0 = score32(fn, v0, mx, inv_sum);
         v1 = per > 1 ? score32(fn, v1, mx, inv_sum) : 0.f;
         if (fn == DSV4_SCORE_SOFTMAX) off *= v0 + v1;
+        off += (2.f * x + 10.f) * kU * (v0 + v1);  // its sum belongs to all of them
       }
-      off += 2.f * blur + 256.f * kU * (fabsf(v0) + fabsf(v1));
       float best = v0 + v1;
       if (!(best == best)) best = -INFINITY;
-      const float worst_off = warp_max(off < INFINITY ? off : 0.f);
-      uint32_t gk = g < a.n_group && i == 0 ? (order_of(best + 0.f) & ~31u) | (31u - (uint32_t)g) : 0u;
+      const float worst_off = __uint_as_float(__reduce_max_sync(kAll, off < INFINITY ? __float_as_uint(off) : 0u));
+      const uint32_t which = 31u >> log_lanes;  // the bits of a group's number
+      uint32_t gk = g < a.n_group && i == 0 ? (order_of(best + 0.f) & ~which) | (which - (uint32_t)g) : 0u;
       unsigned kept = 0;
       uint32_t last = 0;
       for (int j = 0; j < a.topk_group; ++j) {
         last = __reduce_max_sync(kAll, gk);
         if (gk == last) gk = 0u;
-        kept |= 1u << (31u - (last & 31u));
+        kept |= 1u << (which - (last & which));
       }
       const uint32_t next = __reduce_max_sync(kAll, gk);
-      const float vl = value_of(last & ~31u), vn = value_of(next & ~31u);
-      // 2^-17: the five bits of the group; an infinite score or bias says nothing about the others
-      if (!(vl - vn > 2.f * worst_off + 8e-6f * fabsf(vn) + 1e-37f) || !(blur < INFINITY)) {
+      const float vl = value_of(last & ~which), vn = value_of(next & ~which);
+      // 2^-23: what the bits of the number left out; an infinite score or bias says nothing about the others
+      if (!(vl - vn > 2.f * worst_off + 1.2e-7f * (float)(which + 1) * fabsf(vn) + 1e-37f) || !(blur < INFINITY)) {
         uint32_t places = 0;
 #pragma unroll
         for (int j = 0; j < kN; ++j)
           if (key[j] != 0u && !(value(key[j]) + fabsf(value(key[j])) * cut + 1e-37f < second - 2.f * blur))
-            places |= 1u << (whole ? ((int)(low - (key[j] & low)) - e0) >> log_lanes : (int)(key[j] & low));
-        kept = groups_of<T>(a, row, log_lanes, places, (double)mx);
+            places |= 1u << (whole ? ((int)(low - (key[j] & low)) - e0) >> shift : (int)(key[j] & low));
+        kept = groups_of<T>(a, row, log_lanes, e0, shift, places, (double)mx);
       }
       if (!((kept >> g) & 1u)) {
 #pragma unroll
@@ -381,27 +419,39 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
     }
 
     // lane j keeps the j-th key and its expert; the one behind the last shows how sure that is
-    uint32_t mine_key = 0u, behind = 0u;
-    int mine = 0;
+    uint32_t mine_key = 0u, behind = 0u, owners = 0u;
+    const uint32_t* rest = list;
+    if constexpr (kN >= kListed) {
+#pragma unroll
+      for (int j = 2; j < kN; ++j) list[32 * (j - 2)] = key[j];
+    }
     auto take = [&](int j) {
       const uint32_t best = __reduce_max_sync(kAll, key[0]);
-      const int owner = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+      const uint32_t equal = __ballot_sync(kAll, key[0] == best);  // the lowest lane's is taken
       if (lane == j) {
         mine_key = best;
-        mine = owner;
+        owners = equal;
       }
-      if (lane == owner) {
+      if ((equal & upto) == self) {
+        if constexpr (kN >= kListed) {
+          key[0] = key[1];
+          key[1] = *rest;
+          rest += 32;
+        } else {
 #pragma unroll
-        for (int v = 0; v + 1 < kN; ++v) key[v] = key[v + 1];
-        key[kN - 1] = 0u;
+          for (int v = 0; v + 1 < kN; ++v) key[v] = key[v + 1];
+          key[kN - 1] = 0u;
+        }
       }
       return best;
     };
     for (int j = 0; j <= a.topk; ++j) behind = take(j);
     auto expert = [&]() {
-      return whole ? (int)(low - (mine_key & low))
-                   : (mine >> log_lanes) * per + (mine & (lanes - 1)) + ((int)(mine_key & low) << log_lanes);
+      const int owner = __ffs(owners) - 1;
+      const int from = kFull ? owner * kN : (owner >> log_lanes) * per + (owner & (lanes - 1));
+      return whole ? (int)(low - (mine_key & low)) : from + ((int)(mine_key & low) << shift);
     };
+    int mine = 0;
     bool doubt = false;
     if (!whole) {
       const uint32_t after = __shfl_down_sync(kAll, mine_key, 1), next_key = lane == a.topk - 1 ? behind : after;
@@ -412,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
       doubt = __any_sync(kAll, doubt);
     }
     if (!doubt) {
-      mine = expert();
+      mine = lane < a.topk ? expert() : 0;
     } else {
       // the order once more in 64 bits, of those that may belong to it: one per lane
       int n = min(a.topk, 32);
@@ -487,7 +537,8 @@ cudaError_t launch_type(const RouteArgs& a, cudaStream_t st) {
   while ((1 << bits) < a.E) ++bits;
   const int need = (a.E / a.n_group + (1 << log_lanes) - 1) >> log_lanes;  // experts of a lane
   const int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
-  const size_t smem = (size_t)kWarps * scratch_of(a.E) * sizeof(double);
+  const int kn = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : 32;
+  const size_t smem = (size_t)kWarps * (scratch_of(a.E) * sizeof(double) + list_of(kn) * sizeof(uint32_t));
   const auto fn = need <= 1 ? pick<T, 1>(a) : need <= 2 ? pick<T, 2>(a) : need <= 4 ? pick<T, 4>(a) : need <= 8 ? pick<T, 8>(a) :
                   need <= 16 ? pick<T, 16>(a) : pick<T, 32>(a);
   if (smem > 48 * 1024) {
@@ -496,7 +547,7 @@ cudaError_t launch_type(const RouteArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (need > 32) return launch(route_wide_kernel<T>, blocks, kWarps * 32, smem, st, a);
-  const int64_t held = (int64_t)sm_count() * ctas_of(need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : 32);
+  const int64_t held = (int64_t)sm_count() * ctas_of(kn);
   return launch(fn, blocks < held ? blocks : held, kWarps * 32, smem, st, a, log_lanes, bits);
 }
 

@@ -174,7 +174,8 @@ def check_route(abi, logits, bias, fn, topk, n_group=1, topk_group=1, renorm=1, 
 ROUTES = [  # T, E, topk, n_group, topk_group
     (1, 1, 1, 1, 1), (3, 2, 2, 1, 1), (65, 8, 3, 1, 1), (64, 256, 6, 1, 1), (129, 256, 8, 8, 4), (33, 60, 4, 1, 1),
     (50, 96, 5, 3, 2), (12, 1023, 8, 3, 2), (5000, 64, 6, 8, 3), (31, 512, 12, 8, 3), (17, 1024, 32, 32, 32), (9, 33, 32, 1, 1), (20, 32, 4, 32, 7), (40, 14, 7, 2, 1),
-    (700, 400, 10, 1, 1)]
+    (700, 400, 10, 1, 1), (77, 128, 6, 4, 2), (19, 256, 32, 32, 4), (21, 288, 18, 32, 2), (13, 620, 20, 31, 1),
+    (9, 512, 32, 16, 1)]                                       # every expert of the groups that stay
 
 
 @pytest.mark.parametrize("fn", ["softmax", "sigmoid", "sqrt_softplus"])
