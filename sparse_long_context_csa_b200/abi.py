@@ -105,7 +105,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                "dsv4_route_experts", "dsv4_expert_mlp"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
+    _find_calls(lib)
     return lib
+
+
+# The calls without ctypes (csrc/binding.cpp): status, or None for arguments that are not for them
+# (raw pointers, and what the functions below refuse); None before load() and without the module.
+_norm = _route = _experts = None
+
+
+def _find_calls(lib) -> None:
+    global _norm, _route, _experts
+    try:
+        from . import _binding
+    except ImportError:
+        return
+
+    def entry(name, tensors, four, sized=0):
+        return _binding.entry(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value, tensors, four, sized)
+    _norm = entry("dsv4_add_rms_norm", 7, 1 << 6)
+    _route = entry("dsv4_route_experts", 4, 1 << 1 | 1 << 2 | 1 << 3)
+    _experts = entry("dsv4_expert_mlp", 8, 1 << 1 | 1 << 2 | 1 << 3, 1)
 
 
 def _ptr(t) -> int | None:
@@ -162,7 +182,7 @@ def _dense(fn: str, stream, *tensors) -> list:
 
 
 def _four_bytes(fn: str, what: str, t) -> None:
-    """ids and weights as torch.topk returns them (int64, the logits' type) are not what the kernels read."""
+    """What torch.topk returns (ids of int64, weights of the logits' type) is not what the kernels read."""
     if t is not None and type(t) is not int and t.element_size() != 4:
         raise Dsv4Error(fn, 1, f"{what} of type {t.dtype} instead of 32 bits")
 
@@ -269,13 +289,23 @@ def dsv4_grouped_out_proj(params, T, groups, dg, hidden, o, wa, wb, u, y, stream
 
 def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=None, stream=None):
     """r = x + residual (res_out), y = rms_norm(r) * weight, and y in e4m3 with a scale per 128 channels."""
-    _check("dsv4_add_rms_norm", load().dsv4_add_rms_norm(
-        ctypes.byref(params), *_dense("dsv4_add_rms_norm", stream, x, residual, weight, res_out, y, yq, yscale)))
+    if stream is None and _norm is not None:
+        st = _norm(params, x, residual, weight, res_out, y, yq, yscale)
+        if st is not None:
+            return _check("dsv4_add_rms_norm", st)
+    args = _dense("dsv4_add_rms_norm", stream, x, residual, weight, res_out, y, yq, yscale)
+    _four_bytes("dsv4_add_rms_norm", "scales", yscale)
+    _check("dsv4_add_rms_norm", load().dsv4_add_rms_norm(ctypes.byref(params), *args))
 
 
 def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
     """The topk experts of each token (ids, in descending order of score + bias) and their weights."""
+    if stream is None and _route is not None:
+        st = _route(params, logits, bias, ids, weights)
+        if st is not None:
+            return _check("dsv4_route_experts", st)
     args = _dense("dsv4_route_experts", stream, logits, bias, ids, weights)
+    _four_bytes("dsv4_route_experts", "bias", bias)
     _four_bytes("dsv4_route_experts", "ids", ids)
     _four_bytes("dsv4_route_experts", "weights", weights)
     _check("dsv4_route_experts", load().dsv4_route_experts(ctypes.byref(params), *args))
@@ -287,9 +317,14 @@ def dsv4_expert_mlp_workspace_bytes(params: Dsv4MoeParams) -> int:
 
 def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, ws_bytes=None, stream=None):
     """The weighted sum of each token's experts' clamped SwiGLU products."""
+    if stream is None and ws_bytes is None and _experts is not None:
+        st = _experts(params, x, x_scale, ids, weights, w13, w2, out, workspace)
+        if st is not None:
+            return _check("dsv4_expert_mlp", st)
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \
         else (ws_bytes or 0)
     *ptrs, stream = _dense("dsv4_expert_mlp", stream, x, x_scale, ids, weights, w13, w2, out, workspace)
+    _four_bytes("dsv4_expert_mlp", "scales", x_scale)
     _four_bytes("dsv4_expert_mlp", "ids", ids)
     _four_bytes("dsv4_expert_mlp", "weights", weights)
     _check("dsv4_expert_mlp", load().dsv4_expert_mlp(ctypes.byref(params), *ptrs, ws_bytes, stream))

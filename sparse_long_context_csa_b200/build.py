@@ -3,14 +3,16 @@
 Usage: python -m sparse_long_context_csa_b200.build [--debug]
 Each .cu file in csrc/ is compiled to an object in _build/ (in parallel), then linked
 into sparse_long_context_csa_b200/libdsv4.so.  Objects are rebuilt when a source or a
-header is newer.
+header is newer.  csrc/binding.cpp becomes the extension module _binding.so beside it.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsv4.so")
+BINDING = os.path.join(PKG, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -34,6 +37,19 @@ def _newest_header() -> float:
     hs = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
     return max((os.path.getmtime(h) for h in hs), default=0.0)
+
+
+def _build_binding(hdr: float) -> None:
+    src = os.path.join(CSRC, "binding.cpp")
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) > max(os.path.getmtime(src), hdr):
+        return
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include"),
+           src, "-o", BINDING]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
 
 
 def build(debug: bool = False, verbose: bool = False) -> str:
@@ -65,6 +81,7 @@ def build(debug: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    _build_binding(hdr)
     return LIB
 
 

@@ -1,0 +1,165 @@
+// The call of an entry point from Python without ctypes: a callable that takes the params structure
+// and tensors, checks the tensors (on the current device, contiguous, of 32 bits where the entry
+// point reads 32) and calls the function with their addresses and the current stream's handle.
+// Where anything is out of the ordinary (a raw pointer, a tensor that the kernel could not read)
+// it calls nothing and returns None, and the binding in Python, which says what is wrong, goes on.
+// Through ctypes and the tensors' methods such a call took 5.0 us with its launch, this way
+// 2.9 us.  Tensors are looked at through DLPack's exchange interface.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/dlpack.h>
+
+#include "dsv4.h"
+
+namespace {
+
+constexpr int kMaxTensors = 8;
+
+struct Entry {
+  void* function;
+  int tensors;      // arguments between the params and the stream
+  unsigned four;    // which of them are of 32 bits
+  int sized;        // 1: the bytes of the last one are an argument, behind it
+};
+
+const DLPackExchangeAPI* g_api = nullptr;
+PyTypeObject* g_tensor = nullptr;  // torch.Tensor
+PyObject* g_device = nullptr;      // () -> the current CUDA device
+
+PyObject* attribute(PyObject* o, const char* name) {
+  PyObject* v = o ? PyObject_GetAttrString(o, name) : nullptr;
+  PyErr_Clear();
+  return v;
+}
+
+// What the calls need of torch, once it has been imported; it lives as long as the interpreter.
+bool find_torch() {
+  if (g_api) return true;
+  PyObject* torch = PyDict_GetItemString(PyImport_GetModuleDict(), "torch");
+  PyObject* tensor = attribute(torch, "Tensor");
+  PyObject* capsule = attribute(tensor, "__dlpack_c_exchange_api__");
+  PyObject* c = attribute(torch, "_C");
+  PyObject* device = attribute(c, "_cuda_getDevice");
+  Py_XDECREF(c);
+  if (capsule && device && PyType_Check(tensor) && PyCapsule_IsValid(capsule, "dlpack_exchange_api")) {
+    const auto* api = static_cast<const DLPackExchangeAPI*>(PyCapsule_GetPointer(capsule, "dlpack_exchange_api"));
+    if (api->header.version.major == DLPACK_MAJOR_VERSION && api->dltensor_from_py_object_no_sync && api->current_work_stream) {
+      g_tensor = reinterpret_cast<PyTypeObject*>(tensor);
+      g_device = device;
+      g_api = api;
+      return true;
+    }
+  }
+  Py_XDECREF(device);
+  Py_XDECREF(capsule);
+  Py_XDECREF(tensor);
+  return false;
+}
+
+bool contiguous(const DLTensor& t) {
+  if (!t.strides) return true;
+  for (int i = 0; i < t.ndim; ++i)
+    if (t.shape[i] == 0) return true;
+  int64_t step = 1;
+  for (int i = t.ndim - 1; i >= 0; --i) {
+    if (t.shape[i] != 1 && t.strides[i] != step) return false;
+    step *= t.shape[i];
+  }
+  return true;
+}
+
+// (params, tensor or None, ...) -> status, or None: not for this way.
+PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  const auto* e = static_cast<const Entry*>(PyCapsule_GetPointer(self, nullptr));
+  if (!e) return nullptr;
+  if (n != e->tensors + 1 || !find_torch()) Py_RETURN_NONE;
+  void* p[kMaxTensors];
+  int device = -1;
+  int64_t bytes = 0;
+  for (int i = 0; i < e->tensors; ++i) {
+    PyObject* o = args[i + 1];
+    p[i] = nullptr;
+    if (o == Py_None) continue;
+    if (!PyObject_TypeCheck(o, g_tensor)) Py_RETURN_NONE;
+    DLTensor t;
+    if (g_api->dltensor_from_py_object_no_sync(o, &t) != 0) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    if (t.device.device_type != kDLCUDA || (device >= 0 && t.device.device_id != device) || !contiguous(t)) Py_RETURN_NONE;
+    if (((e->four >> i) & 1u) && t.dtype.bits * t.dtype.lanes != 32) Py_RETURN_NONE;
+    device = t.device.device_id;
+    p[i] = static_cast<char*>(t.data) + t.byte_offset;
+    if (e->sized && i == e->tensors - 1) {
+      bytes = t.dtype.bits * t.dtype.lanes / 8;
+      for (int j = 0; j < t.ndim; ++j) bytes *= t.shape[j];
+    }
+  }
+  if (device < 0) Py_RETURN_NONE;
+  PyObject* now = PyObject_CallNoArgs(g_device);
+  if (!now) return nullptr;
+  const long current = PyLong_AsLong(now);
+  Py_DECREF(now);
+  void* stream = nullptr;
+  if (current != device || g_api->current_work_stream(kDLCUDA, device, &stream) != 0) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  Py_buffer params;
+  if (PyObject_GetBuffer(args[0], &params, PyBUF_SIMPLE) != 0) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  if (params.len != (Py_ssize_t)sizeof(dsv4_moe_params)) {
+    PyBuffer_Release(&params);
+    Py_RETURN_NONE;
+  }
+  using V = void*;
+  int status = 0;
+  Py_BEGIN_ALLOW_THREADS
+  if (e->tensors == 4)
+    status = reinterpret_cast<int (*)(V, V, V, V, V, V)>(e->function)(params.buf, p[0], p[1], p[2], p[3], stream);
+  else if (e->tensors == 7)
+    status = reinterpret_cast<int (*)(V, V, V, V, V, V, V, V, V)>(e->function)(params.buf, p[0], p[1], p[2], p[3], p[4], p[5],
+                                                                               p[6], stream);
+  else
+    status = reinterpret_cast<int (*)(V, V, V, V, V, V, V, V, V, size_t, V)>(e->function)(
+        params.buf, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], (size_t)bytes, stream);
+  Py_END_ALLOW_THREADS
+  PyBuffer_Release(&params);
+  return PyLong_FromLong(status);
+}
+
+void free_entry(PyObject* capsule) { delete static_cast<Entry*>(PyCapsule_GetPointer(capsule, nullptr)); }
+
+PyMethodDef g_call = {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL, nullptr};
+
+// entry(address of the function, tensors, four, sized) -> callable
+PyObject* entry(PyObject*, PyObject* args) {
+  unsigned long long address = 0;
+  Entry e{};
+  if (!PyArg_ParseTuple(args, "KiIi", &address, &e.tensors, &e.four, &e.sized)) return nullptr;
+  if (!address || (e.tensors != 4 && e.tensors != 7 && e.tensors != 8) || (e.sized != 0) != (e.tensors == 8)) {
+    PyErr_SetString(PyExc_ValueError, "no entry point has these arguments");
+    return nullptr;
+  }
+  e.function = reinterpret_cast<void*>(address);
+  Entry* held = new Entry(e);
+  PyObject* capsule = PyCapsule_New(held, nullptr, free_entry);
+  if (!capsule) {
+    delete held;
+    return nullptr;
+  }
+  PyObject* f = PyCFunction_New(&g_call, capsule);
+  Py_DECREF(capsule);
+  return f;
+}
+
+PyMethodDef g_methods[] = {{"entry", entry, METH_VARARGS, "entry(address, tensors, four, sized) -> callable"}, {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", "Calls of libdsv4 with tensors.", -1, g_methods,
+                        nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&g_module); }

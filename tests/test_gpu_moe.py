@@ -547,6 +547,51 @@ def test_two_calls_at_once_with_a_workspace_each(abi):
         assert all(torch.equal(g, w) for g, w in zip(got, want))
 
 
+def test_ways_to_call(abi):
+    """Tensors on the current stream, a stream that is given, raw pointers: the same results; what is refused."""
+    from sparse_long_context_csa_b200 import _binding  # noqa: F401
+    T, E, k = 33, 48, 5
+    p = params(abi, T=T, E=E, topk=k, score_fn=FN["sigmoid"], renorm=1, routed_scale=1.0, logits_dtype=abi.F32)
+    logits = torch.nn.Parameter(torch.randn(T, E, generator=gen(31), device="cuda"))
+    bias = torch.randn(E, generator=gen(32), device="cuda")
+
+    def outputs():
+        return torch.full((T, k), -9, dtype=torch.int32, device="cuda"), torch.full((T, k), -9.0, device="cuda")
+
+    got = []
+    for way in range(4):
+        ids, w = outputs()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        if way == 0:
+            assert abi._route(p, logits, bias, ids, w) == 0
+        elif way == 1:
+            abi.dsv4_route_experts(p, logits, bias, ids, w, stream=side)
+        elif way == 2:
+            abi.dsv4_route_experts(p, logits.data_ptr(), bias.data_ptr(), ids.data_ptr(), w.data_ptr(), stream=side.cuda_stream)
+        else:
+            with torch.cuda.stream(side):
+                assert abi._route(p, logits, bias, ids, w) == 0
+                got.append((ids.clone(), w.clone()))
+            torch.cuda.current_stream().wait_stream(side)
+            continue
+        torch.cuda.current_stream().wait_stream(side)
+        got.append((ids, w))
+    torch.cuda.synchronize()
+    assert int(got[0][0].min()) >= 0
+    for ids, w in got[1:]:
+        assert torch.equal(ids, got[0][0]) and torch.equal(w, got[0][1])
+    ids, w = outputs()
+    for bad in ((logits.t().contiguous().t(), bias, ids, w), (logits, bias.cpu(), ids, w), (logits, bias, ids.long(), w),
+                (logits, bias, ids, w.bfloat16()), (logits, bias.double(), ids, w), (logits.cpu(), bias, ids, w)):
+        with pytest.raises(abi.Dsv4Error):
+            abi.dsv4_route_experts(p, *bad)
+    with pytest.raises(abi.Dsv4Error):
+        abi.dsv4_route_experts(p, logits, bias, None, w)
+    torch.cuda.synchronize()
+    assert int(ids.max()) == -9                                     # a refused call writes nothing
+
+
 def test_no_tokens(abi):
     e = torch.empty(0, device="cuda")
     p = params(abi, T=0, hidden=128, inter=64, E=4, topk=2)

@@ -177,3 +177,18 @@ def test_binding_refuses_ids_and_weights_that_are_not_of_32_bits(abi, monkeypatc
             with pytest.raises(abi.Dsv4Error) as e:
                 call()
             assert e.value.status == ARG and f"{8 * size} bits" in str(e.value)
+
+
+def test_calls_without_ctypes(abi):
+    """What the callables pass on to the functions that say what is wrong, and what they refuse."""
+    import torch
+    from sparse_long_context_csa_b200 import _binding
+    abi.load()
+    p, t = _params(abi), torch.zeros(4, dtype=torch.int32)
+    assert abi._route(p, FAKE, None, FAKE, FAKE) is None                # raw pointers
+    assert abi._route(p, t, None, t, t) is None                         # not on a GPU
+    assert abi._route(p, None, None, None, None) is None
+    assert abi._route(p, t, None, t) is None and abi._route() is None   # arguments are missing
+    for bad in ((0, 4, 0, 0), (FAKE, 3, 0, 0), (FAKE, 9, 0, 0), (FAKE, 8, 0, 0), (FAKE, 4, 0, 1)):
+        with pytest.raises(ValueError):
+            _binding.entry(*bad)
