@@ -393,8 +393,8 @@ dsv4_status dsv4_route_experts(const dsv4_moe_params* params, const void* logits
  *   out[t] = sum_j weights[t,j] * W2_e (silu(min(g, L)) * clamp(u, -L, L)),
  *   g = W13_e[0:inter] x_t,   u = W13_e[inter:2*inter] x_t,   e = ids[t,j],  L = swiglu_limit
  * (no clamp with swiglu_limit 0).  bf16 operands with fp32 accumulation; the product of silu
- * and u is rounded to bf16, what is summed over j is kept in 32 bits.  A shared expert is one
- * more column of ids and weights.
+ * and u is rounded to bf16 (up to three tokens: kept in 32 bits), what is summed over j is kept
+ * in 32 bits.  A shared expert is one more column of ids and weights.
  *
  *   x         [T,hidden] bf16; or e4m3 when x_scale is given: x = q * s, rounded to bf16 (exact
  *             where s is a power of two: dsv4_add_rms_norm with scale_pow2)

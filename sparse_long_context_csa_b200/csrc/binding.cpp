@@ -3,8 +3,8 @@
 // point reads 32) and calls the function with their addresses and the current stream's handle.
 // Where anything is out of the ordinary (a raw pointer, a tensor that the kernel could not read)
 // it calls nothing and returns None, and the binding in Python, which says what is wrong, goes on.
-// Through ctypes and the tensors' methods such a call took 5.0 us with its launch, this way
-// 2.9 us.  Tensors are looked at through DLPack's exchange interface.
+// Through ctypes and the tensors' methods a call of one row's norm takes 5.6 us with its launch, this
+// way 3.1 us.  Tensors are looked at through DLPack's exchange interface.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

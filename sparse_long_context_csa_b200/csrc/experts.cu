@@ -2,7 +2,8 @@
 //   out[t] = sum_j weights[t,j] * W2_e h,  h = silu(g) * u,  g = W1_e x_t,  u = W3_e x_t,  e = ids[t,j]
 // with g <- min(g, limit) and u <- clamp(u, -limit, limit) when a limit is given.
 // The (token, choice) pairs are put in order of their expert; h is rounded to bf16 (the type of
-// the second product's operands), the products of a pair are kept in 32 bits until the sum over j.
+// the second product's operands; with few tokens, on the CUDA cores, it stays in 32 bits), the
+// products of a pair are kept in 32 bits until the sum over j.
 #include <cuda.h>
 #include <cuda_fp8.h>
 
@@ -22,6 +23,7 @@ namespace {
 // Chunks that the pairs are counted and placed in: one CTA each.
 constexpr int kMaxChunks = 64, kOrderThreads = 1024;
 constexpr int64_t kOneCta = 4096;  // pairs that a single CTA orders
+constexpr int kFewPairs = 32;      // pairs that the few-token path takes
 
 struct Layout {
   size_t offs, slot_row, counts, h, yp, total;
@@ -34,7 +36,7 @@ Layout layout(int64_t T, int hidden, int inter, int E, int topk) {
   l.slot_row = up((size_t)(E + 1) * 4);
   l.counts = l.slot_row + up((size_t)n * 4);
   l.h = l.counts + (n > kOneCta ? up((size_t)kMaxChunks * E * 4) : 0);
-  l.yp = l.h + up((size_t)n * inter * 2);
+  l.yp = l.h + up((size_t)n * inter * (n <= kFewPairs ? 4 : 2));  // few tokens: fp32
   l.total = l.yp + up((size_t)n * hidden * 4);
   return l;
 }
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(ExpertArgs a, 
 // 85 us with a meeting at every stage).
 // More tokens than three go through the tensor cores: four of six experts take 181 us there and
 // 278 us here, where the rows of more than kFewRows pairs of an expert are streamed again.
-constexpr int kFewPairs = 32, kFewTokens = 3, kFewWarps = 8, kFewRows = 2, kFlush = 32;
+constexpr int kFewTokens = 3, kFewWarps = 8, kFewRows = 2, kFlush = 32;
 constexpr int kFewThreads = (kFewWarps + 1) * 32;
 constexpr uint32_t kFewRing = 96 * 1024;
 constexpr int kFewStages = 8;    // at most
@@ -618,7 +620,7 @@ constexpr int few_batch() { return (kUp ? 4 : 8) / kP; }
 // warp; kR of the pairs at a time.
 template <bool kUp, int kP, int kR>
 __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& fs, uint8_t* smem, FewShared* sh, FewWalk& at,
-                                           int row0, int count, unsigned mine, __nv_bfloat16* h, int c0) {
+                                           int row0, int count, unsigned mine, float* h, int c0) {
   constexpr int kNR = kUp ? 2 : 1, kBatch = few_batch<kUp, kP>(), kV = kBatch * kNR * kR, kPer = 32 / kV;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   static_assert(kBatch * kFewWarps <= kFlush && kV <= 32 && 2 * kFewRows >= kNR * kR, "a stage's parts fit FewShared::part");
@@ -640,11 +642,20 @@ __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& 
 #pragma unroll
       for (int q = 0; q < kP; ++q) {
         const int i = piece + 32 * q;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < K8) {
-          if (!kUp) {
-            v = reinterpret_cast<const uint4*>(h)[(int64_t)slot * K8 + i];
-          } else {
+        if (!kUp) {
+          float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+          if (i < K8) {
+            const float4* row = reinterpret_cast<const float4*>(h) + ((int64_t)slot * K8 + i) * 2;
+            lo = row[0];
+            hi = row[1];
+          }
+          x[r][q][0] = pair_of(lo.x, lo.y);
+          x[r][q][1] = pair_of(lo.z, lo.w);
+          x[r][q][2] = pair_of(hi.x, hi.y);
+          x[r][q][3] = pair_of(hi.z, hi.w);
+        } else {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (i < K8) {
             const int64_t t = slot / a.topk;
             if (a.x_scale)
               v = dequantise(static_cast<const uint2*>(a.x)[t * K8 + i],
@@ -652,10 +663,10 @@ __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& 
             else
               v = static_cast<const uint4*>(a.x)[t * K8 + i];
           }
-        }
-        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[r][q][j] = pair_of(words[j]);
+          for (int j = 0; j < 4; ++j) x[r][q][j] = pair_of(words[j]);
+        }
       }
     }
     for (int i0 = 0; i0 < count; i0 += flush) {
@@ -720,7 +731,7 @@ __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& 
               gate = gate > a.limit ? a.limit : gate;  // a NaN stays one
               u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
             }
-            h[(int64_t)slot * a.inter + row0 + i0 + i] = __float2bfloat16_rn(__fdividef(gate, 1.f + __expf(-gate)) * u);
+            h[(int64_t)slot * a.inter + row0 + i0 + i] = __fdividef(gate, 1.f + __expf(-gate)) * u;
           } else {
             sh->sum[(row0 + i0 + i - c0) * kFewTokens + slot / a.topk] += a.weights[slot] * d[0];
           }
@@ -732,7 +743,7 @@ __device__ __forceinline__ bool few_expert(const ExpertArgs& a, const FewShape& 
 }
 
 template <bool kUp, int kP>
-__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(ExpertArgs a, __nv_bfloat16* h) {
+__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(ExpertArgs a, float* h) {
   constexpr int kNR = kUp ? 2 : 1, kBatch = few_batch<kUp, kP>();
   extern __shared__ __align__(1024) uint8_t smem[];
   FewShared* sh = reinterpret_cast<FewShared*>(smem + kFewRing);
@@ -911,8 +922,9 @@ cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t st) {
     // both CTAs of an SM at once
     if ((e = cudaFuncSetAttribute(up, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(down, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
-    if ((e = launch(up, grid, kFewThreads, up_smem, st, a, h)) != cudaSuccess) return e;
-    return launch(down, grid, kFewThreads, down_smem, st, a, h);
+    float* h32 = reinterpret_cast<float*>(ws + l.h);
+    if ((e = launch(up, grid, kFewThreads, up_smem, st, a, h32)) != cudaSuccess) return e;
+    return launch(down, grid, kFewThreads, down_smem, st, a, h32);
   }
   if (n <= kOneCta) {
     e = launch(order_kernel, 1, kOrderThreads, 0, st, a.ids, n, n, a.E, nullptr, offs, slot_row);

@@ -292,7 +292,7 @@ def experts_inputs(T, hidden, inter, E, topk, seed, x8=None, spread=1.0):
     return x, scale, ids, w, w13, w2
 
 
-def experts_reference(x, scale, ids, w, w13, w2, limit, inexact):
+def experts_reference(x, scale, ids, w, w13, w2, limit, inexact, rounded=True):
     """The formula in 64 bits over (token, choice) pairs, one expert at a time, and the error
     bound of the module docstring (torch on the GPU: the oracle's loop over tokens is compared
     with it below)."""
@@ -314,7 +314,7 @@ def experts_reference(x, scale, ids, w, w13, w2, limit, inexact):
             g, u = g.clamp(max=limit), u.clamp(-limit, limit)
         silu = g * torch.sigmoid(g)
         h = silu * u
-        dh = 1.1 * u.abs() * dg + silu.abs() * du + 1.1 * dg * du + (12 * U + BF) * h.abs()
+        dh = 1.1 * u.abs() * dg + silu.abs() * du + 1.1 * dg * du + (12 * U + (BF if rounded else 0)) * h.abs()
         b = w2[e].double()
         y = h @ b.T
         dy = dh @ b.abs().T + (f + 2) * U * ((h.abs() + dh) @ b.abs().T)
@@ -340,7 +340,8 @@ def check_experts(abi, ins, limit=0.0, inexact=False):
     out = run_experts(abi, ins, limit)
     abi.dsv4_device_check()
     assert bool((out[T:] == 5).all())
-    ref, tol = experts_reference(*ins, limit, inexact)
+    few = T <= 3 and ins[2].numel() <= 32 and max(ins[4].shape[2], ins[5].shape[2]) <= 8192  # h stays in 32 bits
+    ref, tol = experts_reference(*ins, limit, inexact, not few)
     err = (out[:T].double() - ref).abs()
     assert bool((err <= tol).all()), f"worst {float((err / tol).max()):.2f} of the bound"
     return out[:T], ref
