@@ -161,9 +161,94 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormArgs a, int per) {
   }
 }
 
-// Any width, element by element: a warp has whole groups of 128 channels, four per lane.  kG > 0: at
-// most kG groups per warp, kept in registers over the reduction; 0: the row is read a second time.
-// kW of a CTA's eight warps have a row.
+// Rows that are not whole 16-byte pieces, without the 8-bit form.  Behind its first `head` channels a
+// row is on a 16-byte boundary: n pieces are read and written whole, the channels before and
+// behind them by a thread each.  A CTA (or, with `per` = 32, a warp) takes every stride-th row, a
+// multiple of kN, so that its rows have one head and its weights stay in registers; the next row
+// is on its way while one is finished.
+constexpr int kShiftThreads = 512;
+constexpr int kShiftHeld = 1024;  // threads that an SM holds at once
+template <typename T, int kV>
+__global__ void __launch_bounds__(kShiftThreads) norm_shift_kernel(NormArgs a, int per) {
+  constexpr int kN = Piece<T>::kN;
+  __shared__ float part[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = per == 32 ? lane : threadIdx.x;
+  const int rows = per == 32 ? blockDim.x >> 5 : 1;
+  const int64_t stride = (int64_t)gridDim.x * rows;
+  int64_t row = (int64_t)blockIdx.x * rows + (per == 32 ? warp : 0);
+  const int b = (int)(row * a.hidden % kN), head = min((kN - b) % kN, a.hidden);
+  const int n = (a.hidden - head) / kN, behind = head + n * kN;
+  // this thread's channel outside the pieces: threads 0 .. kN - 1 before them, the next kN behind
+  int alone = i0 < kN ? i0 : behind + i0 - kN;
+  if (i0 < kN ? i0 >= head : i0 >= 2 * kN || alone >= a.hidden) alone = -1;
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.residual);
+  wait_for_previous();
+  float w[kV][kN], w_alone = alone >= 0 ? to_f32<T>(static_cast<const T*>(a.weight)[alone]) : 0.f;
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      w[v][j] = i0 + v * per < n ? to_f32<T>(static_cast<const T*>(a.weight)[head + (i0 + v * per) * kN + j]) : 0.f;
+  uint4 vx[kV], vr[kV];
+  T ax = from_f32<T>(0.f), ar = ax;
+  auto load = [&](int64_t at) {
+    const int64_t base = at * a.hidden;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      vx[v] = vr[v] = make_uint4(0, 0, 0, 0);
+      if (i0 + v * per >= n) continue;
+      vx[v] = reinterpret_cast<const uint4*>(x + base + head)[i0 + v * per];
+      if (res) vr[v] = reinterpret_cast<const uint4*>(res + base + head)[i0 + v * per];
+    }
+    if (alone >= 0) {
+      ax = x[base + alone];
+      if (res) ar = res[base + alone];
+    }
+  };
+  auto store = [&](void* out, int64_t base, const float (*f)[kN], float f_alone) {
+    T* p = static_cast<T*>(out) + base;
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      if (i0 + v * per < n) reinterpret_cast<uint4*>(p + head)[i0 + v * per] = Piece<T>::pack(f[v]);
+    if (alone >= 0) p[alone] = from_f32<T>(f_alone);
+  };
+  if (row < a.T) load(row);
+  for (int turn = 0; row < a.T; row += stride, turn ^= 1) {
+    const int64_t base = row * a.hidden;
+    float r[kV][kN], r_alone = to_f32<T>(ax) + to_f32<T>(ar), sq = r_alone * r_alone;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      float f[kN];
+      Piece<T>::unpack(vx[v], r[v]);
+      Piece<T>::unpack(vr[v], f);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        r[v][j] += f[j];
+        sq = fmaf(r[v][j], r[v][j], sq);
+      }
+    }
+    if (row + stride < a.T) load(row + stride);
+    if (a.res_out) store(a.res_out, base, r, r_alone);
+    sq = warp_sum(sq);
+    if (per > 32) {  // the other half of `part` is read by whoever is still at the row before
+      if (lane == 0) part[turn][warp] = sq;
+      __syncthreads();
+      sq = warp_sum(lane < (per >> 5) ? part[turn][lane] : 0.f);
+    }
+    const float inv_rms = rsqrtf(sq / (float)a.hidden + a.eps);
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) r[v][j] = r[v][j] * inv_rms * w[v][j];
+    store(a.y, base, r, r_alone * inv_rms * w_alone);
+  }
+}
+
+// Any width, element by element (with the 8-bit form, and rows too wide for the kernel above): a
+// warp has whole groups of 128 channels, four per lane.  kG > 0: at most kG groups per warp, kept in
+// registers over the reduction; 0: the row is read a second time.  kW of a CTA's eight warps have a
+// row.
 template <typename T, int kG, int kW>
 __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   __shared__ float part[8];
@@ -244,10 +329,24 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
   }
 }
 
+template <typename T, int kV>
+cudaError_t launch_shift(const NormArgs& a, cudaStream_t st) {
+  const int n = a.hidden / Piece<T>::kN, per = n <= 32 * kV ? 32 : ((n + kV - 1) / kV + 31) / 32 * 32, rows = per == 32 ? 8 : 1;
+  const int64_t blocks = ((int64_t)a.T + rows - 1) / rows, held = (int64_t)sm_count() * (kShiftHeld / (per * rows)) / 8 * 8;
+  return launch(norm_shift_kernel<T, kV>, blocks < held ? blocks : held, per * rows, 0, st, a, per);
+}
+
 template <typename T>
 cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
-  // Up to 2048 channels the row stays in registers (16384 x 333 bf16: 15.4 us, 29.6 in two passes of a
-  // CTA per row; 3001 x 1111 fp32: 8.1 and 8.6 us).
+  // Without the 8-bit form: as few pieces a thread as there are threads for, up to 16 channels
+  // (16384 x 1111 bf16 with a residual: 28.0 us with one, 31.8 with two; element by element 45.8;
+  // 4000 x 12001, of 32 channels a thread: 156 us, element by element 136).
+  const int n = a.hidden / Piece<T>::kN;
+  if (!a.yq && n <= kShiftThreads) return launch_shift<T, 1>(a, st);
+  if (!a.yq && n <= 2 * kShiftThreads) return launch_shift<T, 2>(a, st);
+  if (!a.yq && n <= 4 * kShiftThreads && sizeof(T) == 4) return launch_shift<T, 4>(a, st);
+  // With it, up to 2048 channels the row stays in registers (16384 x 333 bf16: 19.2 us, 36.2 in two
+  // passes of a CTA per row; 16384 x 1111: 58.1 and 70.1 us).
   if (a.hidden <= 4 * kScaleGroup) return launch(norm_any_kernel<T, 4, 1>, ((int64_t)a.T + 7) / 8, 256, 0, st, a);
   if (a.hidden <= 8 * kScaleGroup) return launch(norm_any_kernel<T, 4, 2>, ((int64_t)a.T + 3) / 4, 256, 0, st, a);
   if (a.hidden <= 16 * kScaleGroup) return launch(norm_any_kernel<T, 2, 8>, a.T, 256, 0, st, a);

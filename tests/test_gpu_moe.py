@@ -87,7 +87,7 @@ def check_norm(x, residual, weight, eps, res_out, y, q, s, pow2):
 
 NORM_SHAPES = [(1, 4096), (3, 1), (5, 7), (2, 31), (4, 128), (7, 129), (9, 1111), (2, 640), (33, 2048), (17, 8192), (130, 512),
                (2, 8200), (1, 16384), (3, 20001), (1000, 72), (21, 333), (9, 700), (5, 2047), (6, 2049), (600, 256), (3, 32768),
-               (2, 40000)]
+               (2, 40000), (2500, 1111), (10000, 37), (700, 5001), (400, 8191)]                 # more rows than are held at once
 
 
 @pytest.mark.parametrize("T,hidden", NORM_SHAPES)
@@ -115,7 +115,7 @@ def test_norm(abi, T, hidden, dtype):
 
 @pytest.mark.parametrize("T,hidden,dtype", [(5, 4096, torch.bfloat16), (6, 129, torch.float32), (3, 8200, torch.bfloat16),
                                             (9, 333, torch.bfloat16), (3, 5001, torch.bfloat16), (2, 40000, torch.bfloat16),
-                                            (3, 1999, torch.float32)])
+                                            (3, 1999, torch.float32), (1200, 1111, torch.bfloat16), (9000, 99, torch.float32)])
 def test_norm_in_place(abi, T, hidden, dtype):
     """The residual stream updated where it lies, and y written over x."""
     g = gen(9)
