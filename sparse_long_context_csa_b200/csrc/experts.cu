@@ -24,6 +24,10 @@ namespace {
 constexpr int kMaxChunks = 64, kOrderThreads = 1024;
 constexpr int64_t kOneCta = 4096;  // pairs that a single CTA orders
 constexpr int kFewPairs = 32;      // pairs that the few-token path takes
+// Pairs that the gather puts in order by itself, one launch less (4 tokens, 2 of 8 experts of 1024 x
+// 512: 18.1 us, 19.4 with a kernel for the order; 384 pairs of 64: 54.6 and 55.6; 1020 pairs no faster,
+// 4096 pairs 4 us slower).
+constexpr int64_t kPlaced = 512;
 
 struct Layout {
   size_t offs, slot_row, counts, h, yp, total;
@@ -407,12 +411,35 @@ __device__ __forceinline__ uint4 dequantise(uint2 q, float s) {
 // times 16 bytes per lane, and writes it to all of its places (of 2048 tokens or more), or to one
 // (of fewer, for more warps): in the order of the rows, x is read again for every choice once it
 // no longer fits L2 beside what is written (8192 x 4096, 6 choices: 127 us instead of 94).
+// kPlace (a few pairs): the first E + 1 warps find the experts' first rows, the others their pair's
+// row, each by a look at all ids; nothing is put in order before, and splits is topk.
 constexpr int kGatherWarps = 8, kUnroll = 8, kPiece = 32 * kUnroll;
-__global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(ExpertArgs a, int pieces, int splits, const int32_t* slot_row,
-                                                                  __nv_bfloat16* xp) {
+template <bool kPlace>
+__global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(ExpertArgs a, int pieces, int splits, int32_t* offs,
+                                                                  int32_t* slot_row, __nv_bfloat16* xp) {
   wait_for_previous();
   const int lane = threadIdx.x & 31, per = pieces * splits;
-  const int64_t unit = (int64_t)blockIdx.x * kGatherWarps + (threadIdx.x >> 5), t = unit / per;
+  int64_t unit = (int64_t)blockIdx.x * kGatherWarps + (threadIdx.x >> 5);
+  // The pairs of the experts before e, and those of e before pair i.
+  auto row_of = [&](int e, int i) {
+    const int n = a.T * a.topk;
+    int sum = 0;
+#pragma unroll 4
+    for (int j = lane; j < n; j += 32) {
+      const int id = a.ids[j];
+      sum += (id >= 0 && id < e) || (id == e && j < i);
+    }
+    return __reduce_add_sync(0xffffffffu, sum);
+  };
+  if (kPlace) {
+    if (unit <= a.E) {
+      const int first = row_of((int)unit, 0);
+      if (lane == 0) offs[unit] = first;
+      return;
+    }
+    unit -= a.E + 1;
+  }
+  const int64_t t = unit / per;
   if (t >= a.T) return;
   const int rest = (int)(unit - t * per), split = rest / pieces, i0 = (rest - split * pieces) * kPiece + lane;
   const int n = a.hidden / 8;
@@ -436,7 +463,15 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(ExpertArgs a,
     for (int u = 0; u < kUnroll; ++u) v[u] = src[min(i0 + 32 * u, n - 1)];
   }
   for (int j = split; j < a.topk; j += splits) {
-    const int r = slot_row[t * a.topk + j];
+    const int64_t i = t * a.topk + j;
+    int r;
+    if (kPlace) {
+      const int e = a.ids[i];
+      r = is_expert(e, a.E) ? row_of(e, (int)i) : -1;
+      if (lane == 0) slot_row[i] = r;  // every piece's warp the same
+    } else {
+      r = slot_row[i];
+    }
     if (r < 0) continue;
     uint4* dst = reinterpret_cast<uint4*>(xp + (int64_t)r * a.hidden);
 #pragma unroll
@@ -926,19 +961,23 @@ cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t st) {
     if ((e = launch(up, grid, kFewThreads, up_smem, st, a, h32)) != cudaSuccess) return e;
     return launch(down, grid, kFewThreads, down_smem, st, a, h32);
   }
-  if (n <= kOneCta) {
-    e = launch(order_kernel, 1, kOrderThreads, 0, st, a.ids, n, n, a.E, nullptr, offs, slot_row);
-  } else {
-    const int64_t chunk = (n + kMaxChunks - 1) / kMaxChunks, chunks = (n + chunk - 1) / chunk;
-    int32_t* counts = reinterpret_cast<int32_t*>(ws + l.counts);
-    e = launch(count_kernel, chunks, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts);
-    if (e != cudaSuccess) return e;
-    e = launch(order_kernel, chunks, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts, offs, slot_row);
-  }
-  if (e != cudaSuccess) return e;
   const int pieces = (a.hidden / 8 + kPiece - 1) / kPiece, splits = a.T >= 2048 ? 1 : a.topk;
   const int64_t units = (int64_t)a.T * pieces * splits;
-  e = launch(gather_kernel, (units + kGatherWarps - 1) / kGatherWarps, kGatherWarps * 32, 0, st, a, pieces, splits, slot_row, xp);
+  if (n <= kPlaced) {
+    e = launch(gather_kernel<true>, (units + a.E + kGatherWarps) / kGatherWarps, kGatherWarps * 32, 0, st, a, pieces, splits, offs, slot_row, xp);
+  } else {
+    if (n <= kOneCta) {
+      e = launch(order_kernel, 1, kOrderThreads, 0, st, a.ids, n, n, a.E, nullptr, offs, slot_row);
+    } else {
+      const int64_t chunk = (n + kMaxChunks - 1) / kMaxChunks, chunks = (n + chunk - 1) / chunk;
+      int32_t* counts = reinterpret_cast<int32_t*>(ws + l.counts);
+      e = launch(count_kernel, chunks, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts);
+      if (e != cudaSuccess) return e;
+      e = launch(order_kernel, chunks, kOrderThreads, 0, st, a.ids, n, chunk, a.E, counts, offs, slot_row);
+    }
+    if (e != cudaSuccess) return e;
+    e = launch(gather_kernel<false>, (units + kGatherWarps - 1) / kGatherWarps, kGatherWarps * 32, 0, st, a, pieces, splits, offs, slot_row, xp);
+  }
   if (e != cudaSuccess) return e;
   if ((e = launch_gemm<0>(a, xp, n, offs, h, st)) != cudaSuccess) return e;
   if ((e = launch_gemm<1>(a, h, n, offs, yp, st)) != cudaSuccess) return e;

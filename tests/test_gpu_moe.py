@@ -355,6 +355,7 @@ EXPERTS = [  # T, hidden, inter, E, topk
     (2, 4112, 4112, 3, 2), (3, 8192, 272, 4, 3), (1, 8208, 64, 3, 2), (2, 64, 8208, 3, 2),  # widths at the few-token path's ends
     (3, 512, 256, 2, 2), (4, 512, 256, 2, 2), (3, 16, 16, 2, 11), (1, 48, 16, 40, 33),      # tokens and pairs at its ends
     (272, 256, 128, 1, 1), (511, 128, 64, 1, 1), (600, 192, 80, 511, 7), (600, 192, 80, 512, 7), (1025, 128, 32, 1, 4),
+    (512, 64, 16, 9, 1), (513, 64, 16, 9, 1), (256, 2064, 32, 1000, 2), (128, 4112, 16, 2, 4),  # pairs put in order by the gather or before it
     (1030, 2064, 32, 4, 3), (2050, 2064, 16, 3, 2), (4100, 4112, 16, 2, 2)]                 # rows wider than a CTA, and than L2 keeps
 
 
