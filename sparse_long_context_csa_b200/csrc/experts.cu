@@ -924,7 +924,8 @@ cudaError_t launch_gemm(const ExpertArgs& a, const void* rows, int64_t n, const 
   if (!ok) return cudaErrorInvalidValue;
   p.stages = gemm_smem(kStages, a.E) <= kSmemMost ? kStages : kStages - 1;  // 7 of up to 511 experts
   const size_t smem = gemm_smem(p.stages, a.E);
-  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<kPass>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the same value in every call: another thread's may come between this and the launch
+  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<kPass>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
   if (e != cudaSuccess) return e;
   return launch(gemm_kernel<kPass>, sm_count() / 2 * 2, kGemmThreads, smem, st, mw, maps, p);
 }
@@ -952,8 +953,9 @@ cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t st) {
     const auto down = a.inter <= kFewWidth / 2 ? few_kernel<false, 2> : few_kernel<false, 4>;
     const size_t up_smem = kFewRing + sizeof(FewShared);
     const size_t down_smem = up_smem + (size_t)(a.hidden / grid + 1) * kFewTokens * 4;
-    if ((e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)up_smem)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)down_smem)) != cudaSuccess) return e;
+    const size_t most = up_smem + (size_t)(kFewWidth / grid + 1) * kFewTokens * 4;  // of any call, see launch_gemm
+    if ((e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)) != cudaSuccess) return e;
     // both CTAs of an SM at once
     if ((e = cudaFuncSetAttribute(up, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(down, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;

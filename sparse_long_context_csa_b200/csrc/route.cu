@@ -541,11 +541,7 @@ cudaError_t launch_type(const RouteArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)kWarps * (scratch_of(a.E) * sizeof(double) + list_of(kn) * sizeof(uint32_t));
   const auto fn = need <= 1 ? pick<T, 1>(a) : need <= 2 ? pick<T, 2>(a) : need <= 4 ? pick<T, 4>(a) : need <= 8 ? pick<T, 8>(a) :
                   need <= 16 ? pick<T, 16>(a) : pick<T, 32>(a);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(need <= 32 ? (const void*)fn : (const void*)route_wide_kernel<T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  static_assert(kWarps * (kMaxExperts * sizeof(double) + list_of(32) * sizeof(uint32_t)) <= 48 * 1024, "");
   if (need > 32) return launch(route_wide_kernel<T>, blocks, kWarps * 32, smem, st, a);
   const int64_t held = (int64_t)sm_count() * ctas_of(kn);
   return launch(fn, blocks < held ? blocks : held, kWarps * 32, smem, st, a, log_lanes, bits);

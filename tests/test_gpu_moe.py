@@ -549,6 +549,27 @@ def test_two_calls_at_once_with_a_workspace_each(abi):
         assert all(torch.equal(g, w) for g, w in zip(got, want))
 
 
+@pytest.mark.parametrize("shapes", [[(600, 192, 80, 511, 7), (600, 192, 80, 512, 7)], [(3, 8192, 272, 4, 3), (2, 144, 80, 5, 3)]])
+def test_two_threads_at_once(abi, shapes):
+    """Calls that need different amounts of shared memory, by threads that do not wait for each other."""
+    from concurrent.futures import ThreadPoolExecutor
+    ins = [experts_inputs(*s, 40 + i) for i, s in enumerate(shapes)]
+    want = [run_experts(abi, i) for i in ins]
+    torch.cuda.synchronize()
+
+    def work(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ws = torch.empty(want[k].numel() * 64 + (1 << 24), dtype=torch.uint8, device="cuda")
+            out = [run_experts(abi, ins[k], ws=ws) for _ in range(200)]
+            torch.cuda.current_stream().synchronize()
+        return out
+
+    with ThreadPoolExecutor(2) as pool:
+        for got, w in zip(pool.map(work, range(2)), want):
+            assert all(torch.equal(g, w) for g in got)
+    abi.dsv4_device_check()
+
+
 def test_ways_to_call(abi):
     """Tensors on the current stream, a stream that is given, raw pointers: the same results; what is refused."""
     from sparse_long_context_csa_b200 import _binding  # noqa: F401
