@@ -284,10 +284,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
   const int e0 = kFull ? lane * kN : g * per + i, shift = kFull ? 0 : log_lanes;
   // 16-bit logits without a bias are whole in a key's upper half, and the expert's index in the
   // lower one puts equal ones in order; otherwise a key gives up the bits of the place in the lane.
+  // The lower half of a 16-bit value's key is zeros, of one below zero ones, which is what the index
+  // took the place of: `value` gives the logit itself, where otherwise it gives the lowest value with
+  // these upper bits.
   const bool whole = !a.bias && sizeof(T) == 2;
   const int bits = whole ? index_bits : kPlace;
   const uint32_t low = (1u << bits) - 1, lowest = order_of(-INFINITY) & ~low;
-  auto value = [&](uint32_t k) { return (k & ~low) == lowest ? -INFINITY : value_of(k & ~low); };
+  auto value = [&](uint32_t k) {
+    if ((k & ~low) == lowest) return -INFINITY;
+    return value_of(whole && k < 0x80000000u ? k | low : k & ~low);
+  };
   const float cut = __int_as_float((127 + bits - 23) << 23);  // what a key leaves out, of the value
 
   const uint32_t self = 1u << lane, upto = self | (self - 1);

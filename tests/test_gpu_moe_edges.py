@@ -1,0 +1,70 @@
+"""The norm, the routing and the experts at the ends of their ranges: against the fp64 oracle
+(oracle/moe_oracle.py), with the bounds that tests/test_gpu_moe.py derives where none is given."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe_oracle as O
+from test_gpu_moe import FN, abi, check_route, f64, gen, params  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+FNS = ["softmax", "sigmoid", "sqrt_softplus"]
+
+
+# ------------------------------------------------------------------ groups of negative 16-bit logits
+
+def close_sums(fn, n):
+    """n times two pairs of bf16 logits below zero whose scores' sums are closer than a bf16 logit's last
+    bits but further than 64 bits can blur: [n, 2, 2], the larger sum first."""
+    step = np.arange(128, 256, dtype=np.float64)
+    v = -np.concatenate([step * 2.0 ** e for e in (-8, -7, -6, -5)])           # -0.5 .. -8
+    s = np.exp(v) if fn == "softmax" else O.score(fn, v)
+    i, j = np.triu_indices(len(v), 1)
+    total = s[i] + s[j]
+    at = np.argsort(total)
+    gap = np.diff(total[at]) / total[at][1:]
+    some = np.random.default_rng(3).permutation(np.flatnonzero((gap > 2e-8) & (gap < 3e-5)))[:n]
+    lo, hi = at[some], at[some + 1]
+    return np.stack([np.stack([v[i[hi]], v[j[hi]]], 1), np.stack([v[i[lo]], v[j[lo]]], 1)], 1)
+
+
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("E,n_group", [(256, 8), (1024, 8), (60, 4)])
+def test_groups_of_negative_16_bit_logits(abi, fn, E, n_group):
+    """Without a bias, where the two best of two groups are below zero and their sums nearly equal."""
+    T, per = 400, E // n_group
+    pairs = close_sums(fn, T)
+    assert len(pairs) == T
+    rng = np.random.default_rng(E)
+    logits = np.full((T, E), -30.0)
+    for t in range(T):
+        groups = rng.choice(n_group, 2, replace=False)
+        for g, two in zip(groups, pairs[t]):
+            logits[t, g * per + rng.choice(per, 2, replace=False)] = rng.permutation(two)
+    if fn == "sigmoid":
+        logits[0] = -30.0
+        logits[0, [3, 7]] = -2.984375, -1.6328125
+        logits[0, [per + 1, per + 5]] = -2.265625, -2.015625
+    x = torch.from_numpy(logits).cuda().bfloat16()
+    assert np.array_equal(f64(x), logits)
+    check_route(abi, x, None, fn, 3, n_group, 1)
+
+
+@pytest.mark.parametrize("fn", FNS)
+def test_groups_of_many_negative_16_bit_logits(abi, fn):
+    T, E, n_group, kept, k = 200_000, 1024, 8, 4, 4
+    x = (-6 + torch.randn(T, E, generator=gen(17), device="cuda")).bfloat16()
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    abi.dsv4_route_experts(params(abi, T=T, E=E, topk=k, n_group=n_group, topk_group=kept, score_fn=FN[fn], logits_dtype=abi.BF16), x, None,
+                           ids, w)
+    for a in range(0, T, 20_000):                       # the formula in 64 bits
+        l = x[a:a + 20_000].double()
+        s = l.softmax(1) if fn == "softmax" else l.sigmoid() if fn == "sigmoid" else torch.log1p(l.exp()).sqrt()
+        two = s.unflatten(1, (n_group, -1)).sort(2, descending=True).values[:, :, :2].sum(2)
+        best = two.sort(dim=1, descending=True, stable=True).indices[:, :kept]
+        keep = torch.zeros_like(two, dtype=torch.bool).scatter_(1, best, True).repeat_interleave(E // n_group, 1)
+        want = torch.where(keep, l, -torch.inf).sort(dim=1, descending=True, stable=True).indices[:, :k]
+        wrong = (ids[a:a + 20_000] != want).any(1)
+        assert not bool(wrong.any()), f"{int(wrong.sum())} tokens"
