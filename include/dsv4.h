@@ -375,7 +375,7 @@ dsv4_status dsv4_add_rms_norm(const dsv4_moe_params* params, const void* x, cons
  * renorm, times routed_scale: the bias chooses, it does not weigh.
  * The order is that of c in exact arithmetic: choices whose 32-bit values are too close to
  * tell are decided in 64 bits.  A NaN c counts as -inf; a logit of -inf has score 0 (all
- * logits -inf: all scores 0).
+ * logits -inf: all scores 0).  In the weights a score below 2^-126 counts as 0.
  *
  *   logits   [T,E] of logits_dtype
  *   bias     [E] f32 or NULL

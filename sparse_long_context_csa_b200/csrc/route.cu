@@ -188,8 +188,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
 __device__ __forceinline__ float score32(int fn, float l, float mx, float inv_sum) {
   if (fn == DSV4_SCORE_SIGMOID) return rcp_fast(1.f + exp_fast(-l));
   if (fn == DSV4_SCORE_SOFTMAX) return mx == -INFINITY ? 0.f : exp_fast(l - mx) * inv_sum;
+  // e^(l/2), not its square, decides where fp32 ends: below -17 it is the score itself, as
+  // log(1 + e) = e (1 - e / 2 + ..) there, which is 1e-8 of it off at most
+  const float root = exp_fast(-0.5f * fabsf(l));
+  if (l < -17.f) return root;
   // log(1 + e) = 2 atanh(z), z = e / (2 + e) <= 1/3; the terms left out are below 2e-8 of the sum
-  const float e = exp_fast(-fabsf(l)), z = e * rcp_fast(2.f + e), q = z * z;
+  const float e = root * root, z = e * rcp_fast(2.f + e), q = z * z;
   float s = fmaf(q, 1.f / 13.f, 1.f / 11.f);
   s = fmaf(q, s, 1.f / 9.f);
   s = fmaf(q, s, 1.f / 7.f);

@@ -68,3 +68,30 @@ def test_groups_of_many_negative_16_bit_logits(abi, fn):
         want = torch.where(keep, l, -torch.inf).sort(dim=1, descending=True, stable=True).indices[:, :k]
         wrong = (ids[a:a + 20_000] != want).any(1)
         assert not bool(wrong.any()), f"{int(wrong.sum())} tokens"
+
+
+# ------------------------------------------------------------------ scores near fp32's lower end
+
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("E,topk,n_group,kept", [(64, 6, 1, 1), (256, 8, 8, 4), (1023, 8, 3, 2)])
+def test_sqrt_softplus_of_very_negative_logits(abi, E, topk, n_group, kept, renorm):
+    """sqrt(log(1 + e^l)) is about e^(l/2): 1e-19 and less, but not nothing beside the 1e-20 of the sum."""
+    T = 60
+    for k, (dt, bias) in enumerate([(torch.float32, None), (torch.bfloat16, None), (torch.float32, torch.zeros(E, device="cuda")),
+                                    (torch.bfloat16, torch.zeros(E, device="cuda"))]):
+        l = -85 - 25 * torch.rand(T, E, generator=gen(40 + k + E), device="cuda")
+        l[0] = -90.0
+        l[1] = torch.linspace(-10, -24, E, device="cuda")              # across the change of the formula
+        check_route(abi, l.to(dt), bias, "sqrt_softplus", topk, n_group, kept, renorm)
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_sqrt_softplus_groups_of_very_negative_logits(abi, dt, biased):
+    """Two scores of e^-43.75 are more than one of e^-43.25."""
+    E, n_group, per = 64, 4, 16
+    l = torch.full((3, E), -200.0, device="cuda")
+    l[:, 0], l[:, per], l[:, per + 1] = -86.5, -87.5, -87.5
+    l[1, 0] = -86.0
+    l[2, 2 * per:2 * per + 2] = -87.25
+    check_route(abi, l.to(dt), torch.zeros(E, device="cuda") if biased else None, "sqrt_softplus", 2, n_group, 1, 0)
