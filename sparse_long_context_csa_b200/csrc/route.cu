@@ -47,6 +47,18 @@ __device__ __forceinline__ double warp_sum64(double v) {
   return v;
 }
 
+// The largest logit of a row without one above -inf: -inf, or NaN where it holds one (maxima pass over a
+// NaN; in other rows the softmax's sum shows it).
+template <typename T>
+__device__ __noinline__ float largest_of_none(const T* row, int E) {
+  bool nan = false;
+  for (int e = threadIdx.x & 31; e < E; e += 32) {
+    const float l = to_f32<T>(row[e]);
+    nan |= l != l;
+  }
+  return __any_sync(kAll, nan) ? __int_as_float(0x7fffffff) : -INFINITY;
+}
+
 // The larger value of the warp, the lower index among equals; index kNone: no value.
 constexpr int kNone = 1 << 30;
 __device__ __forceinline__ void warp_best(double& v, int& at) {
@@ -70,6 +82,7 @@ __device__ __noinline__ int choose64(const RouteArgs& a, const T* row, double* c
     for (int e = lane; e < a.E; e += 32) mx = fmax(mx, (double)to_f32<T>(row[e]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(kAll, mx, o));
+    if (mx == -INFINITY) mx = (double)largest_of_none<T>(row, a.E);
     for (int e = lane; e < a.E; e += 32) sum += exp((double)to_f32<T>(row[e]) - mx);
     sum = warp_sum64(sum);
   }
@@ -334,6 +347,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(kN)) route_kernel(RouteAr
 #pragma unroll
       for (int j = 0; j < kN; ++j) mx = fmaxf(mx, l[j]);
       mx = warp_max(mx);
+      if (mx == -INFINITY) mx = largest_of_none<T>(static_cast<const T*>(a.logits) + t * a.E, a.E);
       sum = 0.f;
 #pragma unroll
       for (int j = 0; j < kN; ++j) sum += kFull || j < count ? exp_fast(l[j] - mx) : 0.f;
@@ -514,6 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_wide_kernel(RouteArgs a) {
   if (a.score_fn == DSV4_SCORE_SOFTMAX) {
     for (int e = lane; e < a.E; e += 32) mx = fmaxf(mx, to_f32<T>(row[e]));
     mx = warp_max(mx);
+    if (mx == -INFINITY) mx = largest_of_none<T>(row, a.E);
     for (int e = lane; e < a.E; e += 32) sum += exp_fast(to_f32<T>(row[e]) - mx);
     sum = warp_sum(sum);
   }

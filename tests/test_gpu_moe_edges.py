@@ -95,3 +95,24 @@ def test_sqrt_softplus_groups_of_very_negative_logits(abi, dt, biased):
     l[1, 0] = -86.0
     l[2, 2 * per:2 * per + 2] = -87.25
     check_route(abi, l.to(dt), torch.zeros(E, device="cuda") if biased else None, "sqrt_softplus", 2, n_group, 1, 0)
+
+
+# ------------------------------------------------------------------ a softmax of NaN
+
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("E,n_group,kept", [(40, 1, 1), (64, 4, 2), (1023, 3, 1)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_softmax_of_nan(abi, dt, E, n_group, kept, renorm):
+    """A NaN makes every score of its row NaN, whatever stands beside it; the rows around it stay."""
+    inf, nan = float("inf"), float("nan")
+    logits = torch.randn(7, E, generator=gen(50), device="cuda")
+    logits[1] = nan
+    logits[2] = -inf
+    logits[2, E // 2] = nan                                       # nothing else but -inf
+    logits[3, 1] = nan
+    logits[4] = -inf
+    logits[5, 2] = inf
+    bias = torch.linspace(0, 1, E, device="cuda")
+    for b in (None, bias):
+        with np.errstate(invalid="ignore"):
+            check_route(abi, logits.to(dt), b, "softmax", 5, n_group, kept, renorm)
