@@ -415,7 +415,8 @@ dsv4_status dsv4_expert_mlp(const dsv4_moe_params* params, const void* x, const 
                             const float* weights, const void* w13, const void* w2, void* out, void* workspace,
                             size_t ws_bytes, void* stream);
 
-/* Bytes of workspace dsv4_expert_mlp needs (a pure function of T, hidden, inter, E and topk;
+/* Bytes of workspace dsv4_expert_mlp needs (a pure function of T, hidden, inter, E and topk, which
+ * never falls where one of them grows: a workspace for the largest batch serves every smaller one;
  * 0 for sizes that it refuses). */
 size_t dsv4_expert_mlp_workspace_bytes(const dsv4_moe_params* params);
 

@@ -40,7 +40,10 @@ Layout layout(int64_t T, int hidden, int inter, int E, int topk) {
   l.slot_row = up((size_t)(E + 1) * 4);
   l.counts = l.slot_row + up((size_t)n * 4);
   l.h = l.counts + (n > kOneCta ? up((size_t)kMaxChunks * E * 4) : 0);
-  l.yp = l.h + up((size_t)n * inter * (n <= kFewPairs ? 4 : 2));  // few tokens: fp32
+  // bf16, or of up to kFewPairs pairs fp32; every part grows with every size, so that the workspace of a
+  // larger call serves a smaller one
+  const size_t few = (size_t)(n < kFewPairs ? n : kFewPairs) * 4, all = (size_t)n * 2;
+  l.yp = l.h + up((few > all ? few : all) * inter);
   l.total = l.yp + up((size_t)n * hidden * 4);
   return l;
 }
