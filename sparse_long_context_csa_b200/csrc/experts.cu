@@ -156,6 +156,7 @@ struct GemmParams {
   int N;        // output channels (inter, hidden)
   int K;        // reduction length
   int E;
+  int rows;     // of `out`, which all offsets are held to
   int stages;   // of the ring
   float limit;
   const int32_t* offs;  // [E+1] first row of each expert
@@ -185,7 +186,7 @@ struct Cursor {
   int64_t base = 0;          // tiles before expert e
   __device__ Cursor(const int32_t* o, int experts, int weight_tiles) : offs(o), E(experts), wt(weight_tiles) { open(); }
   __device__ void open() {
-    n = e < E ? offs[e + 1] - offs[e] : 0;
+    n = e < E ? max(offs[e + 1] - offs[e], 0) : 0;
     nt = (n + kMaxN - 1) / kMaxN;
   }
   // Tile t (never below the last one asked for): its weight tile, first row and rows; false: none.
@@ -236,7 +237,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     tc::tmem2_relinquish();
   }
   wait_for_previous();
-  for (int e = tid; e <= p.E; e += kGemmThreads) offs[e] = p.offs[e];
+  // Whoever writes to the workspace during the call (a second call that was given the same one, a fill
+  // on another stream) spoils its results and nothing outside: offsets and rows stay within the workspace.
+  for (int e = tid; e <= p.E; e += kGemmThreads) offs[e] = min(max(p.offs[e], 0), p.rows);
   if (tid == 0) {
     tc::prefetch_tensormap(&map_w);
     for (int i = 0; i < kRowMaps; ++i) tc::prefetch_tensormap(&maps.box[i]);
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(ExpertArgs a,
     } else {
       r = slot_row[i];
     }
-    if (r < 0) continue;
+    if ((uint32_t)r >= (uint32_t)(a.T * a.topk)) continue;  // -1: dropped
     uint4* dst = reinterpret_cast<uint4*>(xp + (int64_t)r * a.hidden);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(ExpertArgs a, 
         v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (j0 + j < a.topk) {
           const int r = places[j0 + j];
-          if (r >= 0) {
+          if ((uint32_t)r < (uint32_t)(a.T * a.topk)) {  // -1: dropped
             w[j] = weights[j0 + j];
             v[j] = __ldcs(reinterpret_cast<const float4*>(yp + (int64_t)r * a.hidden) + i);
           }
@@ -903,6 +906,7 @@ cudaError_t launch_gemm(const ExpertArgs& a, const void* rows, int64_t n, const 
   p.N = kPass == 0 ? a.inter : a.hidden;
   p.K = kPass == 0 ? a.hidden : a.inter;
   p.E = a.E;
+  p.rows = (int)n;
   p.limit = a.limit;
   p.offs = offs;
   p.out = out;

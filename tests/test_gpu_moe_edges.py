@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import moe_oracle as O
-from test_gpu_moe import FN, abi, check_route, f64, gen, params  # noqa: F401
+from test_gpu_moe import FN, abi, check_route, experts_inputs, f64, gen, params, run_experts  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,26 @@ def test_softmax_of_nan(abi, dt, E, n_group, kept, renorm):
     for b in (None, bias):
         with np.errstate(invalid="ignore"):
             check_route(abi, logits.to(dt), b, "softmax", 5, n_group, kept, renorm)
+
+
+# ------------------------------------------------------------------ two calls at once
+
+def test_two_calls_at_once_on_streams_of_their_own(abi):
+    """Outputs and workspaces are there, filled, before the streams start and until both have ended."""
+    calls = [experts_inputs(T, 512, 256, 8, 2, T) for T in (600, 30)]
+    want = [run_experts(abi, i).clone() for i in calls]
+    sizes = [abi.dsv4_expert_mlp_workspace_bytes(params(abi, T=i[0].shape[0], hidden=512, inter=256, E=8, topk=2)) for i in calls]
+    spaces = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(20):
+        for t in spaces:
+            t.fill_(255)
+        for t in outs:
+            t.fill_(5.0)
+        torch.cuda.synchronize()
+        for i, o, ws, s in zip(calls, outs, spaces, streams):
+            run_experts(abi, i, out=o, ws=ws, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    abi.dsv4_device_check()
