@@ -121,11 +121,12 @@ def _find_calls(lib) -> None:
     except ImportError:
         return
 
-    def entry(name, tensors, four, sized=0):
-        return _binding.entry(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value, tensors, four, sized)
-    _norm = entry("dsv4_add_rms_norm", 7, 1 << 6)
-    _route = entry("dsv4_route_experts", 4, 1 << 1 | 1 << 2 | 1 << 3)
-    _experts = entry("dsv4_expert_mlp", 8, 1 << 1 | 1 << 2 | 1 << 3, 1)
+    def entry(name, sized=0):
+        holds = sum("-ALFIQX".index(k) << 4 * i for i, k in enumerate(_HOLDS[name]))
+        return _binding.entry(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value, len(_HOLDS[name]), holds, sized)
+    _norm = entry("dsv4_add_rms_norm")
+    _route = entry("dsv4_route_experts")
+    _experts = entry("dsv4_expert_mlp", 1)
 
 
 def _ptr(t) -> int | None:
@@ -181,10 +182,26 @@ def _dense(fn: str, stream, *tensors) -> list:
     return out
 
 
-def _four_bytes(fn: str, what: str, t) -> None:
-    """What torch.topk returns (ids of int64, weights of the logits' type) is not what the kernels read."""
-    if t is not None and type(t) is not int and t.element_size() != 4:
-        raise Dsv4Error(fn, 1, f"{what} of type {t.dtype} instead of 32 bits")
+# What the kernels read and write of each argument: the activations' type (A) or the logits' (L), floats (F)
+# and integers (I) of 32 bits, e4m3 (Q), the experts' rows (X: Q with scales, else A), whatever there is (-).
+_HOLDS = {"dsv4_add_rms_norm": "AAAAAQF", "dsv4_route_experts": "LFIF", "dsv4_expert_mlp": "XFIFAAA-"}
+_TYPES = {F32: ("torch.float32",), BF16: ("torch.bfloat16",), "F": ("torch.float32",), "I": ("torch.int32",),
+          "Q": ("torch.float8_e4m3fn", "torch.uint8")}
+
+
+def _typed(fn: str, params, *tensors) -> None:
+    """The tensors hold what the kernels take them for (what torch.topk returns, int64 ids and weights of the
+    logits' type, is not it).  Of a call without tokens nothing is looked at."""
+    if params.T <= 0:
+        return
+    for kind, t in zip(_HOLDS[fn], tensors):
+        if t is None or type(t) is int:
+            continue
+        if kind == "X":
+            kind = "A" if tensors[1] is None else "Q"
+        want = _TYPES.get({"A": params.dtype, "L": params.logits_dtype}.get(kind, kind))
+        if want and str(t.dtype) not in want:
+            raise Dsv4Error(fn, 1, f"a tensor of type {t.dtype} instead of {want[0]}")
 
 
 def _check(fn: str, st: int) -> None:
@@ -294,7 +311,7 @@ def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=N
         if st is not None:
             return _check("dsv4_add_rms_norm", st)
     args = _dense("dsv4_add_rms_norm", stream, x, residual, weight, res_out, y, yq, yscale)
-    _four_bytes("dsv4_add_rms_norm", "scales", yscale)
+    _typed("dsv4_add_rms_norm", params, x, residual, weight, res_out, y, yq, yscale)
     _check("dsv4_add_rms_norm", load().dsv4_add_rms_norm(ctypes.byref(params), *args))
 
 
@@ -305,9 +322,7 @@ def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
         if st is not None:
             return _check("dsv4_route_experts", st)
     args = _dense("dsv4_route_experts", stream, logits, bias, ids, weights)
-    _four_bytes("dsv4_route_experts", "bias", bias)
-    _four_bytes("dsv4_route_experts", "ids", ids)
-    _four_bytes("dsv4_route_experts", "weights", weights)
+    _typed("dsv4_route_experts", params, logits, bias, ids, weights)
     _check("dsv4_route_experts", load().dsv4_route_experts(ctypes.byref(params), *args))
 
 
@@ -324,9 +339,7 @@ def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, w
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \
         else (ws_bytes or 0)
     *ptrs, stream = _dense("dsv4_expert_mlp", stream, x, x_scale, ids, weights, w13, w2, out, workspace)
-    _four_bytes("dsv4_expert_mlp", "scales", x_scale)
-    _four_bytes("dsv4_expert_mlp", "ids", ids)
-    _four_bytes("dsv4_expert_mlp", "weights", weights)
+    _typed("dsv4_expert_mlp", params, x, x_scale, ids, weights, w13, w2, out, workspace)
     _check("dsv4_expert_mlp", load().dsv4_expert_mlp(ctypes.byref(params), *ptrs, ws_bytes, stream))
 
 

@@ -1,6 +1,6 @@
 // The call of an entry point from Python without ctypes: a callable that takes the params structure
-// and tensors, checks the tensors (on the current device, contiguous, of 32 bits where the entry
-// point reads 32) and calls the function with their addresses and the current stream's handle.
+// and tensors, checks the tensors (on the current device, contiguous, of the types that the entry
+// point reads and writes) and calls the function with their addresses and the current stream's handle.
 // Where anything is out of the ordinary (a raw pointer, a tensor that the kernel could not read)
 // it calls nothing and returns None, and the binding in Python, which says what is wrong, goes on.
 // Through ctypes and the tensors' methods a call of one row's norm takes 5.6 us with its launch, this
@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/dlpack.h>
+#include <string.h>
 
 #include "dsv4.h"
 
@@ -16,10 +17,14 @@ namespace {
 
 constexpr int kMaxTensors = 8;
 
+// What an argument holds: anything, the activations' type, the logits', floats and integers of 32
+// bits, e4m3, the experts' rows (e4m3 with scales, else the activations' type).
+enum Holds : unsigned { kAny, kAct, kLogits, kF32, kI32, kE4m3, kRows };
+
 struct Entry {
   void* function;
   int tensors;      // arguments between the params and the stream
-  unsigned four;    // which of them are of 32 bits
+  unsigned holds;   // of the i-th: 4 bits from 4 i on
   int sized;        // 1: the bytes of the last one are an argument, behind it
 };
 
@@ -69,11 +74,35 @@ bool contiguous(const DLTensor& t) {
   return true;
 }
 
+bool fits(unsigned holds, const DLDataType& t, const dsv4_moe_params& p, bool scaled) {
+  if (t.lanes != 1) return false;
+  if (holds == kRows) holds = scaled ? kE4m3 : kAct;
+  if (holds == kAct || holds == kLogits) {
+    const int32_t type = holds == kAct ? p.dtype : p.logits_dtype;
+    if (type == DSV4_BF16) return t.code == kDLBfloat && t.bits == 16;
+    holds = type == DSV4_F32 ? kF32 : kAny;  // another: for the function to refuse
+  }
+  if (holds == kF32) return t.code == kDLFloat && t.bits == 32;
+  if (holds == kI32) return t.code == kDLInt && t.bits == 32;
+  if (holds == kE4m3) return (t.code == kDLFloat8_e4m3fn || t.code == kDLUInt) && t.bits == 8;
+  return true;
+}
+
 // (params, tensor or None, ...) -> status, or None: not for this way.
 PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   const auto* e = static_cast<const Entry*>(PyCapsule_GetPointer(self, nullptr));
   if (!e) return nullptr;
   if (n != e->tensors + 1 || !find_torch()) Py_RETURN_NONE;
+  Py_buffer params;
+  if (PyObject_GetBuffer(args[0], &params, PyBUF_SIMPLE) != 0) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  dsv4_moe_params sizes;
+  const bool right = params.len == (Py_ssize_t)sizeof(sizes);
+  if (right) memcpy(&sizes, params.buf, sizeof(sizes));
+  PyBuffer_Release(&params);
+  if (!right) Py_RETURN_NONE;
   void* p[kMaxTensors];
   int device = -1;
   int64_t bytes = 0;
@@ -88,7 +117,7 @@ PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
       Py_RETURN_NONE;
     }
     if (t.device.device_type != kDLCUDA || (device >= 0 && t.device.device_id != device) || !contiguous(t)) Py_RETURN_NONE;
-    if (((e->four >> i) & 1u) && t.dtype.bits * t.dtype.lanes != 32) Py_RETURN_NONE;
+    if (sizes.T > 0 && !fits((e->holds >> (4 * i)) & 15u, t.dtype, sizes, args[2] != Py_None)) Py_RETURN_NONE;
     device = t.device.device_id;
     p[i] = static_cast<char*>(t.data) + t.byte_offset;
     if (e->sized && i == e->tensors - 1) {
@@ -106,28 +135,18 @@ PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
-  Py_buffer params;
-  if (PyObject_GetBuffer(args[0], &params, PyBUF_SIMPLE) != 0) {
-    PyErr_Clear();
-    Py_RETURN_NONE;
-  }
-  if (params.len != (Py_ssize_t)sizeof(dsv4_moe_params)) {
-    PyBuffer_Release(&params);
-    Py_RETURN_NONE;
-  }
   using V = void*;
   int status = 0;
   Py_BEGIN_ALLOW_THREADS
   if (e->tensors == 4)
-    status = reinterpret_cast<int (*)(V, V, V, V, V, V)>(e->function)(params.buf, p[0], p[1], p[2], p[3], stream);
+    status = reinterpret_cast<int (*)(V, V, V, V, V, V)>(e->function)(&sizes, p[0], p[1], p[2], p[3], stream);
   else if (e->tensors == 7)
-    status = reinterpret_cast<int (*)(V, V, V, V, V, V, V, V, V)>(e->function)(params.buf, p[0], p[1], p[2], p[3], p[4], p[5],
+    status = reinterpret_cast<int (*)(V, V, V, V, V, V, V, V, V)>(e->function)(&sizes, p[0], p[1], p[2], p[3], p[4], p[5],
                                                                                p[6], stream);
   else
     status = reinterpret_cast<int (*)(V, V, V, V, V, V, V, V, V, size_t, V)>(e->function)(
-        params.buf, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], (size_t)bytes, stream);
+        &sizes, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], (size_t)bytes, stream);
   Py_END_ALLOW_THREADS
-  PyBuffer_Release(&params);
   return PyLong_FromLong(status);
 }
 
@@ -135,11 +154,11 @@ void free_entry(PyObject* capsule) { delete static_cast<Entry*>(PyCapsule_GetPoi
 
 PyMethodDef g_call = {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL, nullptr};
 
-// entry(address of the function, tensors, four, sized) -> callable
+// entry(address of the function, tensors, holds, sized) -> callable
 PyObject* entry(PyObject*, PyObject* args) {
   unsigned long long address = 0;
   Entry e{};
-  if (!PyArg_ParseTuple(args, "KiIi", &address, &e.tensors, &e.four, &e.sized)) return nullptr;
+  if (!PyArg_ParseTuple(args, "KiIi", &address, &e.tensors, &e.holds, &e.sized)) return nullptr;
   if (!address || (e.tensors != 4 && e.tensors != 7 && e.tensors != 8) || (e.sized != 0) != (e.tensors == 8)) {
     PyErr_SetString(PyExc_ValueError, "no entry point has these arguments");
     return nullptr;
@@ -156,7 +175,7 @@ PyObject* entry(PyObject*, PyObject* args) {
   return f;
 }
 
-PyMethodDef g_methods[] = {{"entry", entry, METH_VARARGS, "entry(address, tensors, four, sized) -> callable"}, {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {{"entry", entry, METH_VARARGS, "entry(address, tensors, holds, sized) -> callable"}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", "Calls of libdsv4 with tensors.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

@@ -139,3 +139,42 @@ def test_two_calls_at_once_on_streams_of_their_own(abi):
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
     abi.dsv4_device_check()
+
+
+# ------------------------------------------------------------------ what the tensors hold
+
+def test_tensors_of_another_type_are_refused(abi):
+    """By the calls without ctypes, which leave them to the functions that say what is wrong."""
+    T, h = 4, 256
+    x, w, y = (torch.ones(n, h, device="cuda", dtype=torch.bfloat16) for n in (T, 1, T))
+    q, s = torch.empty(T, h, device="cuda", dtype=torch.float8_e4m3fn), torch.empty(T, 2, device="cuda")
+    p = params(abi, T=T, hidden=h)
+    right = [x, x, w, y.clone(), y, q, s]
+    assert abi._norm(p, *right) == 0 and abi._norm(p, *right[:5], q.view(torch.uint8), s) == 0
+    for i, wrong in ((0, x.float()), (1, x.float()), (2, w.float()), (2, w.half()), (3, y.float()), (4, y.float()), (5, y), (5, q.view(torch.int8)),
+                     (6, s.int()), (6, s.double())):
+        args = [*right[:i], wrong, *right[i + 1:]]
+        assert abi._norm(p, *args) is None
+        with pytest.raises(abi.Dsv4Error) as e:
+            abi.dsv4_add_rms_norm(p, *args)
+        assert e.value.status == 1 and str(wrong.dtype) in str(e.value)
+    ins = experts_inputs(T, 256, 128, 8, 2, 1)
+    p = params(abi, T=T, hidden=256, inter=128, E=8, topk=2)
+    ws = torch.empty(abi.dsv4_expert_mlp_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    right = [*ins, torch.empty_like(ins[0]), ws]
+    assert abi._experts(p, *right) == 0
+    x8, scale = experts_inputs(T, 256, 128, 8, 2, 1, x8="pow2")[:2]
+    assert abi._experts(p, x8, scale, *right[2:]) == 0
+    for over in ({0: x8}, {1: scale}, {0: x8, 1: scale.bfloat16()}, {2: ins[2].float()}, {2: ins[2].long()}, {3: ins[3].int()},
+                 {4: ins[4].float()}, {5: ins[5].float()}, {6: torch.empty(T, 256, device="cuda")}):
+        args = [over.get(i, t) for i, t in enumerate(right)]
+        assert abi._experts(p, *args) is None
+        with pytest.raises(abi.Dsv4Error) as e:
+            abi.dsv4_expert_mlp(p, *args)
+        assert e.value.status == 1
+    p = params(abi, T=T, E=8, topk=2, logits_dtype=abi.BF16)
+    ids, weights = torch.empty(T, 2, dtype=torch.int32, device="cuda"), torch.empty(T, 2, device="cuda")
+    logits = torch.zeros(T, 8, device="cuda")
+    assert abi._route(p, logits, None, ids, weights) is None and abi._route(p, logits.bfloat16(), None, ids, weights) == 0
+    assert abi._route(p, logits.bfloat16(), None, ids.float(), weights) is None
+    torch.cuda.synchronize()

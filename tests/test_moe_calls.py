@@ -63,3 +63,89 @@ def test_the_binding_is_built_where_it_can_be(bare, tmp_path):
         warnings.simplefilter("error")
         assert bare.build() == bare.LIB
     assert (tmp_path / "_binding.so").exists()
+
+
+# ------------------------------------------------------------------ what the tensors hold
+
+class Fake:
+    """A tensor of the current device, as the binding sees it: enough of one for it to be refused."""
+
+    def __init__(self, dtype, shape=(), bits=32):
+        self.dtype, self.shape, self.bits, self.device = dtype, shape, bits, "cuda:0"
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+    def element_size(self):
+        return self.bits // 8
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+
+CALLS = {"dsv4_add_rms_norm": ("x", "residual", "weight", "res_out", "y", "yq", "yscale"),
+         "dsv4_route_experts": ("logits", "bias", "ids", "weights"),
+         "dsv4_expert_mlp": ("x", "x_scale", "ids", "weights", "w13", "w2", "out", "workspace")}
+
+
+def refused(abi, fn, p, **over):
+    """The call with raw addresses but for `over`."""
+    a = {n: FAKE * (i + 1) for i, n in enumerate(CALLS[fn])}
+    if "x_scale" in a:
+        a["x_scale"] = None
+    a.update(over)
+    more = dict(ws_bytes=1) if "workspace" in a else {}
+    with pytest.raises(abi.Dsv4Error) as e:
+        getattr(abi, fn)(p, *a.values(), stream=0, **more)
+    assert e.value.status == ARG, e.value
+    return str(e.value)
+
+
+def test_tensors_of_another_type_are_refused(abi, monkeypatch):
+    """A float32 gamma beside 16-bit activations would be read as twice as many wrong channels, 16-bit
+    rows where 8-bit ones are said to be, float32 ids: each is named before the library is called."""
+    import torch
+    monkeypatch.setattr(abi, "_now", lambda: (0, 0))
+    bf, f32, half, i32, e4 = torch.bfloat16, torch.float32, torch.float16, torch.int32, torch.float8_e4m3fn
+    for dtype, right, wrong in ((abi.BF16, bf, (f32, half, e4, torch.int16)), (abi.F32, f32, (bf, torch.float64, i32))):
+        p = _params(abi, dtype=dtype)
+        for n in ("x", "residual", "weight", "res_out", "y"):
+            for t in wrong:
+                m = refused(abi, "dsv4_add_rms_norm", p, **{n: Fake(t, (1 << 20,))})
+                assert str(t) in m and str(right) in m
+    p = _params(abi)
+    for n, t in (("yq", bf), ("yq", torch.float8_e5m2), ("yscale", bf), ("yscale", i32)):
+        assert str(t) in refused(abi, "dsv4_add_rms_norm", p, **{n: Fake(t, (1 << 20,))})
+    for n, t in (("logits", bf), ("bias", bf), ("bias", i32), ("ids", f32), ("ids", torch.int64), ("weights", i32), ("weights", bf)):
+        assert str(t) in refused(abi, "dsv4_route_experts", p, **{n: Fake(t, (1 << 20,))})
+    refused(abi, "dsv4_route_experts", _params(abi, logits_dtype=abi.BF16), logits=Fake(f32, (1 << 20,)))
+    for n, t in (("x", f32), ("x", e4), ("w13", f32), ("w2", half), ("out", f32), ("ids", f32), ("weights", bf), ("x_scale", bf)):
+        assert str(t) in refused(abi, "dsv4_expert_mlp", p, **{n: Fake(t, (1 << 20,))})
+    refused(abi, "dsv4_expert_mlp", p, x=Fake(bf, (1 << 20,)), x_scale=Fake(f32, (1 << 20,)))  # 16-bit rows with scales
+
+
+def test_tensors_of_the_right_type_get_through(abi, monkeypatch):
+    """As far as the library, which refuses the sizes (nothing is launched)."""
+    import torch
+    monkeypatch.setattr(abi, "_now", lambda: (0, 0))
+    bf, f32, i32 = (Fake(t, (1 << 20,)) for t in (torch.bfloat16, torch.float32, torch.int32))
+    bad = _params(abi, hidden=0, topk=0)
+    for e4 in (Fake(torch.float8_e4m3fn, (1 << 20,)), Fake(torch.uint8, (1 << 20,))):
+        for call in (lambda: abi.dsv4_add_rms_norm(bad, bf, bf, bf, bf, bf, e4, f32, stream=0),
+                     lambda: abi.dsv4_add_rms_norm(_params(abi, hidden=0, dtype=abi.F32), f32, None, f32, None, f32, e4, f32, stream=0),
+                     lambda: abi.dsv4_route_experts(bad, f32, f32, i32, f32, stream=0),
+                     lambda: abi.dsv4_route_experts(_params(abi, topk=0, logits_dtype=abi.BF16), bf, None, i32, f32, stream=0),
+                     lambda: abi.dsv4_expert_mlp(bad, bf, None, i32, f32, bf, bf, bf, f32, ws_bytes=1, stream=0),
+                     lambda: abi.dsv4_expert_mlp(bad, e4, f32, i32, f32, bf, bf, bf, e4, ws_bytes=1, stream=0)):
+            with pytest.raises(abi.Dsv4Error) as e:
+                call()
+            assert e.value.status == SHAPE, e.value
