@@ -189,12 +189,23 @@ _TYPES = {F32: ("torch.float32",), BF16: ("torch.bfloat16",), "F": ("torch.float
           "Q": ("torch.float8_e4m3fn", "torch.uint8")}
 
 
-def _typed(fn: str, params, *tensors) -> None:
+def _elements(fn: str, p) -> tuple:
+    """Elements that the kernels read and write of each argument."""
+    rows, scales = p.T * p.hidden, p.T * -(-p.hidden // 128)
+    if fn == "dsv4_add_rms_norm":
+        return rows, rows, p.hidden, rows, rows, rows, scales
+    if fn == "dsv4_route_experts":
+        return p.T * p.E, p.E, p.T * p.topk, p.T * p.topk
+    matrix = p.E * p.inter * p.hidden
+    return rows, scales, p.T * p.topk, p.T * p.topk, 2 * matrix, matrix, rows, 0
+
+
+def _fit(fn: str, params, *tensors) -> None:
     """The tensors hold what the kernels take them for (what torch.topk returns, int64 ids and weights of the
-    logits' type, is not it).  Of a call without tokens nothing is looked at."""
+    logits' type, is not it), and enough of it.  Of a call without tokens nothing is looked at."""
     if params.T <= 0:
         return
-    for kind, t in zip(_HOLDS[fn], tensors):
+    for kind, t, need in zip(_HOLDS[fn], tensors, _elements(fn, params)):
         if t is None or type(t) is int:
             continue
         if kind == "X":
@@ -202,6 +213,8 @@ def _typed(fn: str, params, *tensors) -> None:
         want = _TYPES.get({"A": params.dtype, "L": params.logits_dtype}.get(kind, kind))
         if want and str(t.dtype) not in want:
             raise Dsv4Error(fn, 1, f"a tensor of type {t.dtype} instead of {want[0]}")
+        if kind != "-" and t.numel() < need:
+            raise Dsv4Error(fn, 1, f"a tensor of {t.numel()} elements where the call has {need}")
 
 
 def _check(fn: str, st: int) -> None:
@@ -311,7 +324,7 @@ def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=N
         if st is not None:
             return _check("dsv4_add_rms_norm", st)
     args = _dense("dsv4_add_rms_norm", stream, x, residual, weight, res_out, y, yq, yscale)
-    _typed("dsv4_add_rms_norm", params, x, residual, weight, res_out, y, yq, yscale)
+    _fit("dsv4_add_rms_norm", params, x, residual, weight, res_out, y, yq, yscale)
     _check("dsv4_add_rms_norm", load().dsv4_add_rms_norm(ctypes.byref(params), *args))
 
 
@@ -322,7 +335,7 @@ def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
         if st is not None:
             return _check("dsv4_route_experts", st)
     args = _dense("dsv4_route_experts", stream, logits, bias, ids, weights)
-    _typed("dsv4_route_experts", params, logits, bias, ids, weights)
+    _fit("dsv4_route_experts", params, logits, bias, ids, weights)
     _check("dsv4_route_experts", load().dsv4_route_experts(ctypes.byref(params), *args))
 
 
@@ -339,7 +352,7 @@ def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, w
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \
         else (ws_bytes or 0)
     *ptrs, stream = _dense("dsv4_expert_mlp", stream, x, x_scale, ids, weights, w13, w2, out, workspace)
-    _typed("dsv4_expert_mlp", params, x, x_scale, ids, weights, w13, w2, out, workspace)
+    _fit("dsv4_expert_mlp", params, x, x_scale, ids, weights, w13, w2, out, workspace)
     _check("dsv4_expert_mlp", load().dsv4_expert_mlp(ctypes.byref(params), *ptrs, ws_bytes, stream))
 
 

@@ -1,6 +1,6 @@
 // The call of an entry point from Python without ctypes: a callable that takes the params structure
 // and tensors, checks the tensors (on the current device, contiguous, of the types that the entry
-// point reads and writes) and calls the function with their addresses and the current stream's handle.
+// point reads and writes, and large enough) and calls the function with their addresses and the current stream's handle.
 // Where anything is out of the ordinary (a raw pointer, a tensor that the kernel could not read)
 // it calls nothing and returns None, and the binding in Python, which says what is wrong, goes on.
 // Through ctypes and the tensors' methods a call of one row's norm takes 5.6 us with its launch, this
@@ -88,6 +88,16 @@ bool fits(unsigned holds, const DLDataType& t, const dsv4_moe_params& p, bool sc
   return true;
 }
 
+// Elements that the entry point of so many tensors reads and writes of the i-th; in floating point, which
+// no sizes overflow.
+double elements(int tensors, int i, const dsv4_moe_params& p) {
+  const double T = p.T, rows = T * p.hidden, scales = T * ((p.hidden + 127LL) / 128), matrix = (double)p.E * p.inter * p.hidden;
+  const double norm[] = {rows, rows, (double)p.hidden, rows, rows, rows, scales};
+  const double route[] = {T * p.E, (double)p.E, T * p.topk, T * p.topk};
+  const double experts[] = {rows, scales, T * p.topk, T * p.topk, 2 * matrix, matrix, rows, 0};
+  return (tensors == 7 ? norm : tensors == 4 ? route : experts)[i];
+}
+
 // (params, tensor or None, ...) -> status, or None: not for this way.
 PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   const auto* e = static_cast<const Entry*>(PyCapsule_GetPointer(self, nullptr));
@@ -118,12 +128,12 @@ PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     }
     if (t.device.device_type != kDLCUDA || (device >= 0 && t.device.device_id != device) || !contiguous(t)) Py_RETURN_NONE;
     if (sizes.T > 0 && !fits((e->holds >> (4 * i)) & 15u, t.dtype, sizes, args[2] != Py_None)) Py_RETURN_NONE;
+    int64_t n = 1;
+    for (int j = 0; j < t.ndim; ++j) n *= t.shape[j];
+    if (sizes.T > 0 && (double)n < elements(e->tensors, i, sizes)) Py_RETURN_NONE;
     device = t.device.device_id;
     p[i] = static_cast<char*>(t.data) + t.byte_offset;
-    if (e->sized && i == e->tensors - 1) {
-      bytes = t.dtype.bits * t.dtype.lanes / 8;
-      for (int j = 0; j < t.ndim; ++j) bytes *= t.shape[j];
-    }
+    if (e->sized && i == e->tensors - 1) bytes = n * (t.dtype.bits * t.dtype.lanes / 8);
   }
   if (device < 0) Py_RETURN_NONE;
   PyObject* now = PyObject_CallNoArgs(g_device);

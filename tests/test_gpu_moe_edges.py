@@ -178,3 +178,29 @@ def test_tensors_of_another_type_are_refused(abi):
     assert abi._route(p, logits, None, ids, weights) is None and abi._route(p, logits.bfloat16(), None, ids, weights) == 0
     assert abi._route(p, logits.bfloat16(), None, ids.float(), weights) is None
     torch.cuda.synchronize()
+
+
+def test_tensors_too_small_for_the_call_are_refused(abi):
+    T, h, E, k = 6, 384, 8, 2
+    p = params(abi, T=T, hidden=h, inter=128, E=E, topk=k)
+    x, w = torch.ones(T, h, device="cuda", dtype=torch.bfloat16), torch.ones(h, device="cuda", dtype=torch.bfloat16)
+    q, s = torch.empty(T, h, device="cuda", dtype=torch.float8_e4m3fn), torch.empty(T, 3, device="cuda")
+    ids, weights = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.ones(T, k, device="cuda")
+    logits, bias = torch.zeros(T, E, device="cuda"), torch.zeros(E, device="cuda")
+    w13, w2 = torch.zeros(E, 256, h, device="cuda").bfloat16(), torch.zeros(E, h, 128, device="cuda").bfloat16()
+    ws = torch.empty(abi.dsv4_expert_mlp_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    for short, call, args in ((abi._norm, abi.dsv4_add_rms_norm, [x, x.clone(), w, torch.empty_like(x), torch.empty_like(x), q, s]),
+                              (abi._route, abi.dsv4_route_experts, [logits, bias, ids, weights]),
+                              (abi._experts, abi.dsv4_expert_mlp, [x, None, ids, weights, w13, w2, torch.empty_like(x), ws]),
+                              (abi._experts, abi.dsv4_expert_mlp, [q, s, ids, weights, w13, w2, torch.empty_like(x), ws])):
+        assert short(p, *args) == 0
+        for i, t in enumerate(args):
+            if t is None:
+                continue
+            less = [*args[:i], t.flatten()[:-1], *args[i + 1:]]
+            if t is not ws:                          # the library says what is wrong with a workspace
+                assert short(p, *less) is None
+            with pytest.raises(abi.Dsv4Error) as e:
+                call(p, *less)
+            assert e.value.status == (7 if t is ws else 1)
+    torch.cuda.synchronize()

@@ -149,3 +149,32 @@ def test_tensors_of_the_right_type_get_through(abi, monkeypatch):
             with pytest.raises(abi.Dsv4Error) as e:
                 call()
             assert e.value.status == SHAPE, e.value
+
+
+def test_tensors_too_small_for_the_call_are_refused(abi, monkeypatch):
+    """What the params say is read and written has to be there; more may be."""
+    import torch
+    monkeypatch.setattr(abi, "_now", lambda: (0, 0))
+    bf, f32, i32, e4 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+    T, h, f, E, k = 5, 272, 48, 16, 2
+    p = _params(abi, T=T, hidden=h, inter=f, E=E, topk=k)
+    sizes = {"dsv4_add_rms_norm": dict(x=(bf, T * h), residual=(bf, T * h), weight=(bf, h), res_out=(bf, T * h), y=(bf, T * h),
+                                       yq=(e4, T * h), yscale=(f32, T * 3)),
+             "dsv4_route_experts": dict(logits=(f32, T * E), bias=(f32, E), ids=(i32, T * k), weights=(f32, T * k)),
+             "dsv4_expert_mlp": dict(x=(bf, T * h), ids=(i32, T * k), weights=(f32, T * k), w13=(bf, E * 2 * f * h), w2=(bf, E * h * f),
+                                     out=(bf, T * h))}
+    for fn, args in sizes.items():
+        for n, (t, need) in args.items():
+            assert str(need) in refused(abi, fn, p, **{n: Fake(t, (need - 1,))})
+    refused(abi, "dsv4_expert_mlp", p, x=Fake(e4, (T * h,)), x_scale=Fake(f32, (T * 3 - 1,)))
+    full = {fn: {n: Fake(t, (need + 1,)) for n, (t, need) in args.items()} for fn, args in sizes.items()}
+    odd = _params(abi, T=T, hidden=h, inter=f, E=E, topk=k, dtype=abi.BF16, eps=-1.0, renorm=2, swiglu_limit=-1.0)
+    for fn, args in full.items():  # through to the library, which refuses a flag and launches nothing
+        if fn == "dsv4_expert_mlp":
+            args = {"x": args.pop("x"), "x_scale": None, **args, "workspace": Fake(torch.uint8, (1,))}
+        more = dict(ws_bytes=1) if "workspace" in args else {}
+        with pytest.raises(abi.Dsv4Error) as e:
+            getattr(abi, fn)(odd, *args.values(), stream=0, **more)
+        assert e.value.status == ARG and "null pointer or bad flag" in str(e.value)
+    huge = _params(abi, T=2 ** 31 - 1, hidden=2 ** 31 - 1, inter=2 ** 31 - 1, E=2 ** 31 - 1)
+    refused(abi, "dsv4_expert_mlp", huge, w13=Fake(bf, (1 << 40,)))
