@@ -268,6 +268,7 @@ def moe_buffers(p: abi.Dsv4MoeParams, device="cuda") -> dict:
         return torch.empty(shape, dtype=dtype, device=device)
 
     o = {"stream": new(p.T, p.hidden), "y": new(p.T, p.hidden), "out": new(p.T, p.hidden),
+         "y32": new(p.T, p.hidden, dtype=torch.float32),  # what the router's product reads
          "logits": new(p.T, p.E, dtype=torch.float32), "ids": new(p.T, p.topk, dtype=torch.int32),
          "weights": new(p.T, p.topk, dtype=torch.float32), "q": None, "q_scale": None,
          "workspace": new(abi.dsv4_expert_mlp_workspace_bytes(p), dtype=torch.uint8)}
@@ -282,10 +283,11 @@ def moe_step(p: abi.Dsv4MoeParams, x: dict, o: dict, stream=None) -> None:
       stream = attn + residual stream, y = rms_norm(stream) * gamma  (with its e4m3 form)
       logits = y router^T, ids and weights by score + bias, out = the experts' weighted products
     x: attn, stream [T,hidden] bf16, gamma [hidden] bf16, router [E,hidden] float32, bias [E] float32
-    or None, w13 [E,2*inter,hidden], w2 [E,hidden,inter] bf16; o: ``moe_buffers``.  The router's
+    or None, w13 [E,2*inter,hidden], w2 [E,hidden,inter] bf16; o: ``moe_buffers``, which the step
+    writes and beside which it allocates nothing.  The router's
     product runs on the current stream, which ``stream``, when given, has to be."""
     abi.dsv4_add_rms_norm(p, x["attn"], x["stream"], x["gamma"], o["stream"], o["y"], o["q"], o["q_scale"], stream=stream)
-    torch.mm(o["y"].float(), x["router"].t(), out=o["logits"])
+    torch.mm(o["y32"].copy_(o["y"]), x["router"].t(), out=o["logits"])
     abi.dsv4_route_experts(p, o["logits"], x["bias"], o["ids"], o["weights"], stream=stream)
     rows, scale = (o["y"], None) if o["q"] is None else (o["q"], o["q_scale"])
     abi.dsv4_expert_mlp(p, rows, scale, o["ids"], o["weights"], x["w13"], x["w2"], o["out"], o["workspace"], stream=stream)

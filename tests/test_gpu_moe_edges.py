@@ -204,3 +204,26 @@ def test_tensors_too_small_for_the_call_are_refused(abi):
                 call(p, *less)
             assert e.value.status == (7 if t is ws else 1)
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ the step
+
+def layer(harness, T, seed=0):
+    p = harness.moe_params(T, 512, 256, 16, 4, n_group=4, topk_group=2, routed_scale=1.5, swiglu_limit=7.0)
+    g = gen(seed)
+    rnd = lambda *sh: torch.randn(sh, generator=g, device="cuda")  # noqa: E731
+    return p, dict(attn=rnd(T, 512).bfloat16(), stream=rnd(T, 512).bfloat16(), gamma=(1 + 0.1 * rnd(512)).bfloat16(),
+                   router=rnd(16, 512) / 512 ** 0.5, bias=0.1 * rnd(16), w13=(rnd(16, 512, 512) / 512 ** 0.5).bfloat16(),
+                   w2=(rnd(16, 512, 256) / 256 ** 0.5).bfloat16())
+
+
+@pytest.mark.parametrize("T", [1, 700])
+def test_a_step_allocates_nothing(abi, T):
+    from sparse_long_context_csa_b200 import harness
+    p, x = layer(harness, T)
+    o = harness.moe_buffers(p)
+    harness.moe_step(p, x, o)                           # the library that PyTorch calls makes its workspace once
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    harness.moe_step(p, x, o)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
