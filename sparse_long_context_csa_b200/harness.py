@@ -284,10 +284,13 @@ def moe_step(p: abi.Dsv4MoeParams, x: dict, o: dict, stream=None) -> None:
       logits = y router^T, ids and weights by score + bias, out = the experts' weighted products
     x: attn, stream [T,hidden] bf16, gamma [hidden] bf16, router [E,hidden] float32, bias [E] float32
     or None, w13 [E,2*inter,hidden], w2 [E,hidden,inter] bf16; o: ``moe_buffers``, which the step
-    writes and beside which it allocates nothing.  The router's
-    product runs on the current stream, which ``stream``, when given, has to be."""
-    abi.dsv4_add_rms_norm(p, x["attn"], x["stream"], x["gamma"], o["stream"], o["y"], o["q"], o["q_scale"], stream=stream)
-    torch.mm(o["y32"].copy_(o["y"]), x["router"].t(), out=o["logits"])
-    abi.dsv4_route_experts(p, o["logits"], x["bias"], o["ids"], o["weights"], stream=stream)
-    rows, scale = (o["y"], None) if o["q"] is None else (o["q"], o["q_scale"])
-    abi.dsv4_expert_mlp(p, rows, scale, o["ids"], o["weights"], x["w13"], x["w2"], o["out"], o["workspace"], stream=stream)
+    writes and beside which it allocates nothing.  All of it runs on ``stream`` (a torch stream or a
+    cudaStream_t as an integer; None: the current one), the router's product too."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()  # 0: a new stream there
+    with torch.cuda.stream(stream):
+        abi.dsv4_add_rms_norm(p, x["attn"], x["stream"], x["gamma"], o["stream"], o["y"], o["q"], o["q_scale"])
+        torch.mm(o["y32"].copy_(o["y"]), x["router"].t(), out=o["logits"])
+        abi.dsv4_route_experts(p, o["logits"], x["bias"], o["ids"], o["weights"])
+        rows, scale = (o["y"], None) if o["q"] is None else (o["q"], o["q_scale"])
+        abi.dsv4_expert_mlp(p, rows, scale, o["ids"], o["weights"], x["w13"], x["w2"], o["out"], o["workspace"])

@@ -227,3 +227,27 @@ def test_a_step_allocates_nothing(abi, T):
     before = torch.cuda.memory_stats()["allocation.all.allocated"]
     harness.moe_step(p, x, o)
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+
+
+@pytest.mark.parametrize("way", ["stream", "handle", "default"])
+def test_a_step_on_a_stream_that_is_not_the_current_one(abi, way):
+    """Behind work that keeps the stream busy for a while: nothing of the step may run ahead of it."""
+    from sparse_long_context_csa_b200 import harness
+    p, x = layer(harness, 300)
+    want, o = harness.moe_buffers(p), harness.moe_buffers(p)
+    harness.moe_step(p, x, want)
+    big = torch.zeros(1 << 28, device="cuda")
+    for t in o.values():
+        if t is not None:
+            t.zero_()
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    where = torch.cuda.default_stream() if way == "default" else side
+    with torch.cuda.stream(where):
+        for _ in range(20):
+            big += 1.0
+    with torch.cuda.stream(other):
+        harness.moe_step(p, x, o, stream=where if way == "stream" else where.cuda_stream)
+    where.synchronize()
+    for n in ("stream", "y", "logits", "ids", "weights", "out"):
+        assert torch.equal(o[n], want[n]), n

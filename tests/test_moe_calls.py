@@ -178,3 +178,43 @@ def test_tensors_too_small_for_the_call_are_refused(abi, monkeypatch):
         assert e.value.status == ARG and "null pointer or bad flag" in str(e.value)
     huge = _params(abi, T=2 ** 31 - 1, hidden=2 ** 31 - 1, inter=2 ** 31 - 1, E=2 ** 31 - 1)
     refused(abi, "dsv4_expert_mlp", huge, w13=Fake(bf, (1 << 40,)))
+
+
+# ------------------------------------------------------------------ the step
+
+@pytest.mark.parametrize("given", ["none", "stream", "handle", "default"])
+def test_a_step_is_on_one_stream(abi, monkeypatch, given):
+    """The router's product between the calls of the library runs on the stream that they run on."""
+    import contextlib
+
+    import torch
+    from sparse_long_context_csa_b200 import harness
+    now, seen = ["current"], []
+
+    class Stream:
+        cuda_stream = 77
+
+    @contextlib.contextmanager
+    def on(stream):
+        before = now[0]
+        if stream is not None:
+            now[0] = stream
+        yield
+        now[0] = before
+
+    def call(*args, stream=None):
+        handle = now[0] if stream is None else stream
+        seen.append(getattr(handle, "cuda_stream", handle))
+
+    mm = torch.mm
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: type("S", (), {"cuda_stream": handle or "a new one"})())
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: type("S", (), {"cuda_stream": 0})())
+    monkeypatch.setattr(torch, "mm", lambda *a, **k: (call(), mm(*a, **k))[1])
+    for n in ("dsv4_add_rms_norm", "dsv4_route_experts", "dsv4_expert_mlp"):
+        monkeypatch.setattr(abi, n, call)
+    p = harness.moe_params(3, 16, 16, 4, 2)
+    o = harness.moe_buffers(p, device="cpu")
+    x = dict(attn=None, stream=None, gamma=None, router=torch.zeros(4, 16), bias=None, w13=None, w2=None)
+    harness.moe_step(p, x, o, **{"none": {}, "stream": dict(stream=Stream()), "handle": dict(stream=77), "default": dict(stream=0)}[given])
+    assert seen == [{"none": "current", "default": 0}.get(given, 77)] * 4
