@@ -318,7 +318,8 @@ dsv4_status dsv4_grouped_out_proj(const dsv4_params* params, int32_t T, int32_t 
 
 /* Sizes of one call of the operators that follow the attention in a decoder layer: the
  * residual stream's norm, the routing to experts and the experts' products.  The caller sets
- * every field that the called entry point names. */
+ * every field that the called entry point names.  With T == 0 the sizes and flags are checked and
+ * no pointer is looked at. */
 typedef struct dsv4_moe_params {
   int32_t T;            /* tokens */
   int32_t hidden;       /* hidden_size */

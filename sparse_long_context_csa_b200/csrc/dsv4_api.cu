@@ -480,6 +480,7 @@ dsv4_status dsv4_add_rms_norm(const dsv4_moe_params* p, const void* x, const voi
   if (bad_dtype(p->dtype)) return DSV4_ERR_DTYPE;
   if (p->T < 0 || p->hidden < 1 || p->hidden > kMaxWidth) return DSV4_ERR_SHAPE;
   if (!(p->eps >= 0.f) || bad_flag(p->scale_pow2)) return DSV4_ERR_ARG;
+  if (p->T == 0) return DSV4_OK;
   if (!x || !weight || (!y && !yq) || (yq && !yscale) || (!yq && yscale)) return DSV4_ERR_ARG;
   const void* ptrs[] = {x, residual, weight, res_out, y, yq, yscale};
   for (const void* q : ptrs)
@@ -503,6 +504,7 @@ dsv4_status dsv4_route_experts(const dsv4_moe_params* p, const void* logits, con
   if (p->topk > p->topk_group * (p->E / p->n_group)) return DSV4_ERR_SHAPE;
   if (p->score_fn < DSV4_SCORE_SOFTMAX || p->score_fn > DSV4_SCORE_SQRT_SOFTPLUS) return DSV4_ERR_ARG;
   if (bad_flag(p->renorm) || !(p->routed_scale == p->routed_scale)) return DSV4_ERR_ARG;
+  if (p->T == 0) return DSV4_OK;
   if (!logits || !ids || !weights) return DSV4_ERR_ARG;
   const void* ptrs[] = {logits, bias, ids, weights};
   for (const void* q : ptrs)
@@ -524,11 +526,11 @@ dsv4_status dsv4_expert_mlp(const dsv4_moe_params* p, const void* x, const float
                             size_t ws_bytes, void* stream) {
   dsv4_status st = check_experts(p);
   if (st != DSV4_OK) return st;
+  if (p->T == 0) return DSV4_OK;
   if (!x || !ids || !weights || !w13 || !w2 || !out || out == x) return DSV4_ERR_ARG;
   const void* ptrs[] = {x, x_scale, ids, weights, w13, w2, out, workspace};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return DSV4_ERR_ALIGN;
-  if (p->T == 0) return DSV4_OK;
   if (!workspace || ws_bytes < dsv4_expert_mlp_workspace_bytes(p)) return DSV4_ERR_WORKSPACE;
   ExpertArgs a{};
   a.T = p->T; a.hidden = p->hidden; a.inter = p->inter; a.E = p->E; a.topk = p->topk; a.limit = p->swiglu_limit;

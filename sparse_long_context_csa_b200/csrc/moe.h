@@ -1,5 +1,5 @@
 // Launchers of the operators that follow the attention in a decoder layer (norm.cu, route.cu,
-// experts.cu).  Arguments arrive validated; each launcher returns the cudaGetLastError() of its
+// experts.cu).  Arguments arrive validated, T > 0; each launcher returns the cudaGetLastError() of its
 // launches.
 #pragma once
 

@@ -251,3 +251,20 @@ def test_a_step_on_a_stream_that_is_not_the_current_one(abi, way):
     where.synchronize()
     for n in ("stream", "y", "logits", "ids", "weights", "out"):
         assert torch.equal(o[n], want[n]), n
+
+
+# ------------------------------------------------------------------ no tokens
+
+def test_tensors_of_no_tokens(abi):
+    """A batch that is empty: torch's tensors of no rows have no address."""
+    from sparse_long_context_csa_b200 import harness
+    for eight_bit in (False, True):
+        p = harness.moe_params(0, 256, 64, 8, 2, eight_bit=eight_bit)
+        o = harness.moe_buffers(p)
+        x = dict(attn=torch.empty(0, 256, device="cuda").bfloat16(), stream=torch.empty(0, 256, device="cuda").bfloat16(),
+                 gamma=torch.ones(256, device="cuda").bfloat16(), router=torch.zeros(8, 256, device="cuda"), bias=torch.zeros(8, device="cuda"),
+                 w13=torch.zeros(8, 128, 256, device="cuda").bfloat16(), w2=torch.zeros(8, 256, 64, device="cuda").bfloat16())
+        before = abi.dsv4_launch_count()
+        harness.moe_step(p, x, o)
+        assert abi.dsv4_launch_count() == before
+    torch.cuda.synchronize()

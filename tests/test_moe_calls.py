@@ -218,3 +218,21 @@ def test_a_step_is_on_one_stream(abi, monkeypatch, given):
     x = dict(attn=None, stream=None, gamma=None, router=torch.zeros(4, 16), bias=None, w13=None, w2=None)
     harness.moe_step(p, x, o, **{"none": {}, "stream": dict(stream=Stream()), "handle": dict(stream=77), "default": dict(stream=0)}[given])
     assert seen == [{"none": "current", "default": 0}.get(given, 77)] * 4
+
+
+# ------------------------------------------------------------------ no tokens
+
+def test_no_tokens_need_no_tensors(abi):
+    """A tensor without rows has no address in torch; the sizes and flags are looked at all the same."""
+    def nothing(names):
+        return {n: None for n in names}
+
+    none = _params(abi, T=0)
+    assert _norm(abi, none, **nothing(("x", "residual", "weight", "res_out", "y", "yq", "yscale"))) == OK
+    assert _route(abi, none, **nothing(("logits", "bias", "ids", "weights"))) == OK
+    assert _experts(abi, none, ws_bytes=0, **nothing(CALLS["dsv4_expert_mlp"])) == OK
+    assert _norm(abi, _params(abi, T=0, hidden=0), x=None) == SHAPE
+    assert _norm(abi, _params(abi, T=0, eps=-1.0), x=None) == ARG
+    assert _route(abi, _params(abi, T=0, topk=0), logits=None) == SHAPE
+    assert _route(abi, _params(abi, T=0, renorm=2), logits=None) == ARG
+    assert _experts(abi, _params(abi, T=0, inter=0), x=None) == SHAPE
