@@ -36,7 +36,10 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, size_t smem,
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-  if (e == cudaSuccess) note_launch(1);
+  if (e == cudaSuccess)
+    note_launch(1);
+  else
+    (void)cudaGetLastError();  // returned here, and not by a later call that asks for the last error
   return e;
 }
 

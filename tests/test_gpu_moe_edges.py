@@ -268,3 +268,25 @@ def test_tensors_of_no_tokens(abi):
         harness.moe_step(p, x, o)
         assert abi.dsv4_launch_count() == before
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ a launch that is refused
+
+def test_a_refused_launch_leaves_no_error_behind(tmp_path):
+    """The runtime keeps a failed call's error until it is asked for, and the attention's launchers ask
+    behind their own launches: an error that stayed would be theirs.  The launch is refused on the host
+    (a CTA of more threads than there can be)."""
+    import subprocess
+    from sparse_long_context_csa_b200 import build
+    (tmp_path / "t.cu").write_text("""
+#include <stdio.h>
+#include "launch.cuh"
+namespace dsv4 { void note_launch(int) { printf("launched "); } }
+__global__ void nothing(int) {}
+int main() {
+  const cudaError_t e = dsv4::launch(nothing, 1, 4096, 0, cudaStream_t(nullptr), 1);
+  printf("%d %d", e != cudaSuccess, cudaGetLastError() == cudaSuccess);
+}
+""")
+    subprocess.run([build.NVCC, *build._flags(False), str(tmp_path / "t.cu"), "-o", str(tmp_path / "t")], check=True)
+    assert subprocess.run([str(tmp_path / "t")], check=True, capture_output=True, text=True).stdout == "1 1"
