@@ -29,13 +29,20 @@ __device__ __forceinline__ float group_scale(float amax, int pow2) {
   return s;
 }
 
-// v / s, by the reciprocal but where that leaves fp32's normal range.
+// v / s.  A power of two within fp32's normal range has an exact reciprocal; of another scale the product
+// with its rounded reciprocal is brought to the quotient by its remainder (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990); the sign is that of the product,
+// for a zero's.  8191 x 4096 bf16: 49.0 us, by `/` 51.5, by the rounded reciprocal alone 48.3, which put two of
+// eight million values a step beside e4m3(v / s).
 template <int kN>
-__device__ __forceinline__ void divide(float (&v)[kN], float s) {
-  if (s >= 0x1p-100f) {
+__device__ __forceinline__ void divide(float (&v)[kN], float s, int pow2) {
+  if (s >= 0x1p-100f && s < INFINITY) {
     const float inv = __frcp_rn(s);
 #pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] *= inv;
+    for (int j = 0; j < kN; ++j) {
+      const float q = v[j] * inv;
+      v[j] = pow2 ? q : copysignf(fmaf(fmaf(-q, s, v[j]), inv, q), q);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < kN; ++j) v[j] /= s;
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormArgs a, int per) {
     for (int o = kScaleGroup / kN / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     const float s = group_scale(__uint_as_float(i < n ? most : 0u), a.scale_pow2);
     if (i >= n) continue;
-    divide(r[v], s);
+    divide(r[v], s, a.scale_pow2);
     if (i % (kScaleGroup / kN) == 0) a.yscale[row * groups + i / (kScaleGroup / kN)] = s;
     uint32_t q[kN / 4];
 #pragma unroll
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
     if (!a.yq) return;
     const float s = group_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, most)), a.scale_pow2);
     if (lane == 0) a.yscale[row * groups + g] = s;
-    divide(v, s);
+    divide(v, s, a.scale_pow2);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = g * kScaleGroup + i * 32 + lane;

@@ -290,3 +290,20 @@ int main() {
 """)
     subprocess.run([build.NVCC, *build._flags(False), str(tmp_path / "t.cu"), "-o", str(tmp_path / "t")], check=True)
     assert subprocess.run([str(tmp_path / "t")], check=True, capture_output=True, text=True).stdout == "1 1"
+
+
+# ------------------------------------------------------------------ the 8-bit form
+
+@pytest.mark.parametrize("T,hidden", [(2048, 4096), (3000, 333), (900, 5001)])
+def test_8_bit_values_are_those_of_the_division(abi, T, hidden):
+    """q = e4m3(y / s), bit for bit: float32 rows hand out the y that q is formed from."""
+    x = torch.randn(T, hidden, generator=gen(T), device="cuda")
+    w = 1 + 0.3 * torch.randn(hidden, generator=gen(T + 1), device="cuda")
+    x[::7, 3], w[9], x[5] = -0.0, 0.0, -0.0                        # zeros of both signs
+    for pow2 in (0, 1):
+        y, q = torch.empty_like(x), torch.empty(T, hidden, dtype=torch.float8_e4m3fn, device="cuda")
+        s = torch.empty(T, -(-hidden // 128), device="cuda")
+        abi.dsv4_add_rms_norm(params(abi, T=T, hidden=hidden, scale_pow2=pow2, dtype=abi.F32), x, None, w, None, y, q, s)
+        want = (y / s.repeat_interleave(128, 1)[:, :hidden]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        wrong = int((q.view(torch.uint8) != want.view(torch.uint8)).sum())
+        assert wrong == 0, f"{wrong} of {T * hidden}"
