@@ -307,3 +307,52 @@ def test_8_bit_values_are_those_of_the_division(abi, T, hidden):
         want = (y / s.repeat_interleave(128, 1)[:, :hidden]).clamp(-448, 448).to(torch.float8_e4m3fn)
         wrong = int((q.view(torch.uint8) != want.view(torch.uint8)).sum())
         assert wrong == 0, f"{wrong} of {T * hidden}"
+
+
+# ------------------------------------------------------------------ weights beside masked logits
+
+def check_weights(abi, logits, bias, fn, topk, n_group=1, topk_group=1, renorm=1, scale=2.5):
+    """Ids and weights with a bound per token, from the logits that it chose.  exp's argument is rounded
+    by u of itself and by the product with log2(e) once more; arguments beyond 104 (where fp32's exp is
+    zero) leave no weight.  A softmax adds the sum's error (argument up to 104 for every term that is
+    not zero) and its chain of E / 32 + 16 additions; 40 u are for exp, log1p, the root, the divisions
+    and the products, as in the other file; renormalised weights have the error of the sum too."""
+    T, E = logits.shape
+    p = params(abi, T=T, E=E, topk=topk, n_group=n_group, topk_group=topk_group, score_fn=FN[fn], renorm=renorm, routed_scale=scale,
+               logits_dtype=abi.F32 if logits.dtype == torch.float32 else abi.BF16)
+    ids, w = torch.empty(T, topk, dtype=torch.int32, device="cuda"), torch.empty(T, topk, device="cuda")
+    abi.dsv4_route_experts(p, logits, bias, ids, w)
+    l, got = f64(logits), f64(w)
+    ref_ids, ref = O.route(l, None if bias is None else f64(bias), fn=fn, topk=topk, n_group=n_group, topk_group=topk_group,
+                           renorm=bool(renorm), routed_scale=scale)
+    np.testing.assert_array_equal(ids.cpu().numpy(), ref_ids)
+    for t in range(T):
+        chosen = l[t][ref_ids[t]]
+        live = ref[t] > 0
+        assert np.all(got[t][~live] == 0), f"token {t}: a weight where there is none"
+        if not live.any():
+            continue
+        arg = chosen[live] - (l[t].max() if fn == "softmax" else 0)
+        every = l[t][np.isfinite(l[t])] - l[t].max() if fn == "softmax" else np.zeros(1)
+        top = min(np.abs(arg).max(), 104.0) + min(np.abs(every).max(), 104.0)
+        rel = 2.0 ** -24 * (40 + 2 * top + E / 32) * (2 if renorm else 1)
+        assert np.all(np.abs(got[t] - ref[t])[live] <= rel * ref[t][live]), f"token {t}: {got[t]} instead of {ref[t]}"
+
+
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_weights_beside_masked_logits(abi, fn, renorm):
+    """Rows of -inf, of the lowest value, with fewer experts left than are chosen, and ordinary ones."""
+    T, E = 8, 40
+    for dt in (torch.float32, torch.bfloat16):
+        logits = torch.randn(T, E, generator=gen(8), device="cuda").to(dt)
+        logits[0] = -float("inf")
+        logits[1, 3:] = -float("inf")
+        logits[2] = torch.finfo(dt).min
+        logits[3, ::2] = torch.finfo(dt).min
+        logits[4, 4:] = torch.finfo(dt).min
+        check_weights(abi, logits, None, fn, 6, renorm=renorm)
+        check_weights(abi, logits, None, fn, 6, 4, 2, renorm)
+        bias = 0.1 * torch.randn(E, generator=gen(9), device="cuda")
+        check_weights(abi, logits, bias, fn, 6, renorm=renorm)
+        check_weights(abi, logits, bias, fn, 6, 4, 2, renorm)
