@@ -27,32 +27,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 }
 
 // One box of a tensor into this CTA's shared memory; the bytes count on the barrier at `bar`
-// (an address in the cluster's window, in either CTA of the pair).
-__device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma2_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma2_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int v, int w,
-                                             uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w), "r"(bar)
-      : "memory");
-}
-
-// The same, and whether the phase of `next` is complete: asked for ahead of the load and looked at
-// behind it.
+// (an address in the cluster's window, in either CTA of the pair).  Returns whether the phase of `next`
+// is complete: asked for ahead of the load and looked at behind it.
 __device__ __forceinline__ bool tma2_load_2d_test(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar,
                                                   uint64_t* next, uint32_t parity) {
   uint32_t ok;
@@ -108,18 +84,6 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// D[tmem of both CTAs] (+)= A B^T, bf16 operands, fp32 accumulation: rows 0-127 of A and the first
-// half of B's rows in the leader's shared memory, the rest at the same offsets in the peer's.  One
-// thread of the leader.
-__device__ __forceinline__ void umma2_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // Arrive once on the barrier at `bar`'s offset in both CTAs when every MMA issued so far is done.
 __device__ __forceinline__ void umma2_commit_both(uint64_t* bar) {
   asm volatile(
@@ -129,8 +93,10 @@ __device__ __forceinline__ void umma2_commit_both(uint64_t* bar) {
       : "memory");
 }
 
-// Four such steps of 16 channels over 64, operands in 128-byte rows, and the commit of them on the
-// barrier at `done`'s offset in both CTAs.  Returns whether the phase of `next` is complete; it is
+// D[tmem of both CTAs] (+)= A B^T, bf16 operands, fp32 accumulation: rows 0-127 of A and the first
+// half of B's rows in the leader's shared memory, the rest at the same offsets in the peer's.  Four steps
+// of 16 channels over 64, operands in 128-byte rows, by one thread of the leader, and the commit of them
+// on the barrier at `done`'s offset in both CTAs.  Returns whether the phase of `next` is complete; it is
 // asked for ahead of the MMAs and looked at behind them (the answer takes 180 clocks, issuing them
 // 340).
 __device__ __forceinline__ bool umma2_f16_step(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
