@@ -185,8 +185,15 @@ def _dense(fn: str, stream, *tensors) -> list:
 # What the kernels read and write of each argument: the activations' type (A) or the logits' (L), floats (F)
 # and integers (I) of 32 bits, e4m3 (Q), the experts' rows (X: Q with scales, else A), whatever there is (-).
 _HOLDS = {"dsv4_add_rms_norm": "AAAAAQF", "dsv4_route_experts": "LFIF", "dsv4_expert_mlp": "XFIFAAA-"}
-_TYPES = {F32: ("torch.float32",), BF16: ("torch.bfloat16",), "F": ("torch.float32",), "I": ("torch.int32",),
-          "Q": ("torch.float8_e4m3fn", "torch.uint8")}
+_types = None
+
+
+def _find_types() -> dict:
+    global _types
+    import torch
+    _types = {F32: (torch.float32,), BF16: (torch.bfloat16,), "F": (torch.float32,), "I": (torch.int32,),
+              "Q": (torch.float8_e4m3fn, torch.uint8)}
+    return _types
 
 
 def _elements(fn: str, p) -> tuple:
@@ -205,13 +212,14 @@ def _fit(fn: str, params, *tensors) -> None:
     logits' type, is not it), and enough of it.  Of a call without tokens nothing is looked at."""
     if params.T <= 0:
         return
+    types = _types or _find_types()
     for kind, t, need in zip(_HOLDS[fn], tensors, _elements(fn, params)):
         if t is None or type(t) is int:
             continue
         if kind == "X":
             kind = "A" if tensors[1] is None else "Q"
-        want = _TYPES.get({"A": params.dtype, "L": params.logits_dtype}.get(kind, kind))
-        if want and str(t.dtype) not in want:
+        want = types.get(params.dtype if kind == "A" else params.logits_dtype if kind == "L" else kind)
+        if want and t.dtype not in want:
             raise Dsv4Error(fn, 1, f"a tensor of type {t.dtype} instead of {want[0]}")
         if kind != "-" and t.numel() < need:
             raise Dsv4Error(fn, 1, f"a tensor of {t.numel()} elements where the call has {need}")
@@ -319,8 +327,8 @@ def dsv4_grouped_out_proj(params, T, groups, dg, hidden, o, wa, wb, u, y, stream
 
 def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=None, stream=None):
     """r = x + residual (res_out), y = rms_norm(r) * weight, and y in e4m3 with a scale per 128 channels."""
-    if stream is None and _norm is not None:
-        st = _norm(params, x, residual, weight, res_out, y, yq, yscale)
+    if _norm is not None:
+        st = _norm(params, x, residual, weight, res_out, y, yq, yscale, stream if stream is None else _stream(stream))
         if st is not None:
             return _check("dsv4_add_rms_norm", st)
     args = _dense("dsv4_add_rms_norm", stream, x, residual, weight, res_out, y, yq, yscale)
@@ -330,8 +338,8 @@ def dsv4_add_rms_norm(params, x, residual, weight, res_out, y, yq=None, yscale=N
 
 def dsv4_route_experts(params, logits, bias, ids, weights, stream=None):
     """The topk experts of each token (ids, in descending order of score + bias) and their weights."""
-    if stream is None and _route is not None:
-        st = _route(params, logits, bias, ids, weights)
+    if _route is not None:
+        st = _route(params, logits, bias, ids, weights, stream if stream is None else _stream(stream))
         if st is not None:
             return _check("dsv4_route_experts", st)
     args = _dense("dsv4_route_experts", stream, logits, bias, ids, weights)
@@ -345,8 +353,8 @@ def dsv4_expert_mlp_workspace_bytes(params: Dsv4MoeParams) -> int:
 
 def dsv4_expert_mlp(params, x, x_scale, ids, weights, w13, w2, out, workspace, ws_bytes=None, stream=None):
     """The weighted sum of each token's experts' clamped SwiGLU products."""
-    if stream is None and ws_bytes is None and _experts is not None:
-        st = _experts(params, x, x_scale, ids, weights, w13, w2, out, workspace)
+    if ws_bytes is None and _experts is not None:
+        st = _experts(params, x, x_scale, ids, weights, w13, w2, out, workspace, stream if stream is None else _stream(stream))
         if st is not None:
             return _check("dsv4_expert_mlp", st)
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None and workspace is not None \

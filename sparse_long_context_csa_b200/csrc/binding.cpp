@@ -1,9 +1,10 @@
 // The call of an entry point from Python without ctypes: a callable that takes the params structure
 // and tensors, checks the tensors (on the current device, contiguous, of the types that the entry
-// point reads and writes, and large enough) and calls the function with their addresses and the current stream's handle.
+// point reads and writes, and large enough) and calls the function with their addresses and the handle of the current stream, or of
+// the one that is given behind them.
 // Where anything is out of the ordinary (a raw pointer, a tensor that the kernel could not read)
 // it calls nothing and returns None, and the binding in Python, which says what is wrong, goes on.
-// Through ctypes and the tensors' methods a call of one row's norm takes 5.6 us with its launch, this
+// Through ctypes and the tensors' methods a call of one row's norm takes 7.2 us with its launch, this
 // way 3.1 us.  Tensors are looked at through DLPack's exchange interface.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -98,11 +99,12 @@ double elements(int tensors, int i, const dsv4_moe_params& p) {
   return (tensors == 7 ? norm : tensors == 4 ? route : experts)[i];
 }
 
-// (params, tensor or None, ...) -> status, or None: not for this way.
+// (params, tensor or None, ..., [handle of a stream or None]) -> status, or None: not for this way.
 PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   const auto* e = static_cast<const Entry*>(PyCapsule_GetPointer(self, nullptr));
   if (!e) return nullptr;
-  if (n != e->tensors + 1 || !find_torch()) Py_RETURN_NONE;
+  PyObject* given = n == e->tensors + 2 && args[n - 1] != Py_None ? args[n - 1] : nullptr;
+  if ((n != e->tensors + 1 && n != e->tensors + 2) || (given && !PyLong_Check(given)) || !find_torch()) Py_RETURN_NONE;
   Py_buffer params;
   if (PyObject_GetBuffer(args[0], &params, PyBUF_SIMPLE) != 0) {
     PyErr_Clear();
@@ -141,7 +143,8 @@ PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   const long current = PyLong_AsLong(now);
   Py_DECREF(now);
   void* stream = nullptr;
-  if (current != device || g_api->current_work_stream(kDLCUDA, device, &stream) != 0) {
+  if (given) stream = PyLong_AsVoidPtr(given);
+  if (current != device || PyErr_Occurred() || (!given && g_api->current_work_stream(kDLCUDA, device, &stream) != 0)) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }

@@ -356,3 +356,31 @@ def test_weights_beside_masked_logits(abi, fn, renorm):
         bias = 0.1 * torch.randn(E, generator=gen(9), device="cuda")
         check_weights(abi, logits, bias, fn, 6, renorm=renorm)
         check_weights(abi, logits, bias, fn, 6, 4, 2, renorm)
+
+
+def test_a_stream_that_is_given(abi):
+    """Without ctypes as well: behind work that keeps it busy, while the current stream has none; what is no
+    stream's handle is left to the function that says so."""
+    T, h = 64, 512
+    p = params(abi, T=T, hidden=h)
+    x, w = torch.randn(T, h, generator=gen(60), device="cuda").bfloat16(), torch.ones(h, device="cuda").bfloat16()
+    want, y = torch.empty_like(x), torch.empty_like(x)
+    assert abi._norm(p, x, None, w, None, want, None, None) == 0
+    big, side = torch.zeros(1 << 28, device="cuda"), torch.cuda.Stream()
+    for way in (side, side.cuda_stream):
+        late = torch.zeros_like(x)
+        y.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                big += 1.0
+            late.copy_(x)
+        abi.dsv4_add_rms_norm(p, late, None, w, None, y, stream=way)
+        side.synchronize()
+        assert torch.equal(y, want)
+    assert abi._norm(p, x, None, w, None, y, None, None, side.cuda_stream) == 0
+    assert abi._norm(p, x, None, w, None, y, None, None, None) == 0
+    assert abi._norm(p, x, None, w, None, y, None, None, 1.5) is None
+    assert abi._norm(p, x, None, w, None, y, None, None, 1 << 80) is None
+    assert abi._norm(p, x, None, w, None, y, None, None, None, None) is None
+    torch.cuda.synchronize()
